@@ -355,6 +355,134 @@ lrkv_status lrkv_value_projection(const lrkv_problem* p, const void* x, int32_t 
                                   lrkv_stream_t stream);
 
 /* ---------------------------------------------------------------------- */
+/* The shared base K/V cache held in 8 bits.                               */
+/* ---------------------------------------------------------------------- */
+
+/*
+ * A base cache of half the size: one 8-bit code per element and one fp32 scale
+ * per block of LRKV_QUANT_BLOCK tokens and KV head, for K and for V apart.  An
+ * element stands for code * scale.  The low-rank caches U stay bf16 (they are
+ * a few percent of the bytes).  The pages keep every cache in bf16; this is the
+ * library's own addition for contexts whose base cache outgrows the memory or
+ * the bandwidth at hand.
+ *
+ *  LRKV_Q_E4M3  fp8 codes (1 sign, 4 exponent, 3 mantissa bits, largest 448):
+ *               about 2^-4 relative error at worst, whatever the element's size
+ *               within its block (channels of unequal size, outliers).
+ *  LRKV_Q_INT8  codes in [-127, 127]: half a step of 1/127 of the block's
+ *               largest magnitude at worst (blocks without outliers).
+ *
+ * Codes: head_dim contiguous; strides in elements (bytes), multiples of 16.
+ * Scales: finite and >= 0.
+ *  Dense  (page_table == NULL): code (s, g, t, e) at s*stride_session +
+ *         g*stride_head + t*stride_token + e; the scale of block j = t / 64 at
+ *         s*scale_stride_session + g*scale_stride_head + j.
+ *  Paged  (page_table != NULL): page p is one block: code (p, g, j, e) at
+ *         p*stride_page + g*stride_head + j*stride_token + e, its scale at
+ *         p*scale_stride_page + g*scale_stride_head.  The page table is the one
+ *         of lrkv_kv_view.
+ */
+typedef enum { LRKV_Q_E4M3 = 0, LRKV_Q_INT8 = 1 } lrkv_qformat;
+#define LRKV_QUANT_BLOCK 64
+
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t stride_session;
+  int64_t stride_head;
+  int64_t stride_token;
+  int64_t scale_stride_session;
+  int64_t scale_stride_head;
+  const int32_t* page_table;
+  int64_t page_table_stride;
+  int64_t stride_page;
+  int64_t scale_stride_page;
+  int32_t page_size;      /* LRKV_QUANT_BLOCK when paged */
+  int32_t num_pages;
+  int32_t format;         /* lrkv_qformat */
+} lrkv_qkv_view;
+
+/* Bytes of workspace lrkv_quantize_kv and lrkv_dequantize_kv need: the status flags. */
+#define LRKV_KV_QUANT_WORKSPACE_BYTES ((size_t)256)
+
+/*
+ * Write new tokens into an 8-bit cache: for every session s of p, rows
+ * [f, f + n) of the cache take rows [0, n) of session s of `src`, with
+ * f = first_rows[s] (0 when NULL) and n = row_counts[s] (T when NULL).
+ *
+ * The cache grows in order: after the call session s holds f + n tokens, and
+ * what stood at later rows of the last block is no longer valid (its codes are
+ * left as they were, their scale may have changed).  For each (block, KV head)
+ * that a session's rows touch, and K and V apart, with amax the largest finite
+ * |x| among the new rows in it:
+ *   need   = e4m3: the smallest power of two at which amax <= 448 need;
+ *            int8: the smallest bf16 number at which amax <= 127 need;
+ *            at least 2^-100
+ *   scale' = need if the block's first row is new, else max(scale, need)
+ *   new codes  = round(x / scale'), nearest, ties to even, saturating
+ *   kept codes = round(code * scale / scale') of the rows before f, when
+ *                scale' differs from scale
+ * A power-of-two e4m3 scale makes both divisions exact, so a growing scale costs
+ * the kept rows nothing but what falls below e4m3's smallest step; int8 codes
+ * are rounded once more.  With scales that this call wrote, every code is the
+ * nearest one to the real quotient; with other scales the e4m3 quotient is
+ * rounded to fp32 first.  An infinity saturates; a NaN becomes e4m3's NaN or
+ * int8's 0; either raises a device flag (lrkv_query_device_status).
+ *   src          bf16, dense or paged (row t of session s is new token t); any
+ *                strides that are multiples of 8 elements, so both a projection's
+ *                [S, T, Hkv, d] and a bf16 cache's [S, Hkv, T, d] order are read
+ *   T            host-side bound on the counts
+ *   dst_rows     row capacity of each session of dst
+ *   first_rows, row_counts   device int32 [S] or NULL
+ *   workspace    device, >= LRKV_KV_QUANT_WORKSPACE_BYTES, zero-filled once
+ * Two sessions that write the same page race: a page being written belongs to
+ * one session.  A session with a negative first row or count, a count above T
+ * or rows past dst_rows is flagged on the device and not written; a block with
+ * a page id out of range (in src or dst) likewise.  p->num_agents, num_q_heads
+ * and rank play no part but must be valid.  T == 0 is a no-op.
+ */
+lrkv_status lrkv_quantize_kv(const lrkv_problem* p, const lrkv_kv_view* src, int32_t T, const lrkv_qkv_view* dst,
+                             int32_t dst_rows, const int32_t* first_rows, const int32_t* row_counts,
+                             void* workspace, size_t workspace_bytes, lrkv_stream_t stream);
+
+/*
+ * Read an 8-bit cache back: rows [0, n) of session s of `dst` (bf16, dense or
+ * paged) take code * scale, rounded to nearest even bf16, of rows [f, f + n) of
+ * session s of `src`; f, n, T and the workspace as in lrkv_quantize_kv.  Rows
+ * of dst past n are left as they were.  The prefill chunk over an 8-bit cache
+ * is this call into a bf16 staging cache, then lrkv_attn_prefill_chunk.
+ *   src_rows     row capacity of each session of src
+ * Sessions and pages out of range are flagged and skipped, as above.
+ */
+lrkv_status lrkv_dequantize_kv(const lrkv_problem* p, const lrkv_qkv_view* src, int32_t src_rows, int32_t T,
+                               const lrkv_kv_view* dst, const int32_t* first_rows, const int32_t* row_counts,
+                               void* workspace, size_t workspace_bytes, lrkv_stream_t stream);
+
+/* Bytes of workspace lrkv_attn_decode_quant needs (whatever the lengths up to
+ * max_seq_len); 0 if the call would refuse the shape. */
+size_t lrkv_decode_quant_workspace_bytes(const lrkv_problem* p, int32_t max_seq_len);
+
+/*
+ * lrkv_attn_decode over an 8-bit base cache:
+ *   out[s,i,h,:] = sum_{t < seq_lens[s]} P[t] (cv[t] sv[t/64] + [t >= a_{s,i}] U_i[t] B_i,g)
+ *   P = softmax(q[s,i,h] . ck[t] sk[t/64] * scale)
+ * with codes c and scales s of the cache.  Other arguments as lrkv_attn_decode.
+ * Numerics: codes enter the tensor cores exactly, as fp16; q exactly (scaled by a
+ * power of two per row); softmax statistics, scores and accumulators in fp32;
+ * the weights enter the value product as fp16 (times the block's value scale,
+ * against a running reference, so no weight of a long context underflows) and
+ * the low-rank product as bf16.  Codes, scales and U rows at or past seq_len and U
+ * rows before a_i may hold anything, NaN included.
+ * Ragged batches are split over the SMs by their actual lengths.
+ */
+lrkv_status lrkv_attn_decode_quant(const lrkv_problem* p, const void* q, const lrkv_qkv_view* kv,
+                                   const int32_t* seq_lens, int32_t max_seq_len, const lrkv_u_view* u,
+                                   const void* b, const int32_t* alora_offsets, void* out, int32_t out_dtype,
+                                   void* workspace, size_t workspace_bytes, lrkv_stream_t stream);
+
+/* ---------------------------------------------------------------------- */
 
 /* Zero-fill a workspace on `stream` (asynchronous). */
 lrkv_status lrkv_workspace_reset(void* workspace, size_t workspace_bytes, lrkv_stream_t stream);
@@ -362,8 +490,8 @@ lrkv_status lrkv_workspace_reset(void* workspace, size_t workspace_bytes, lrkv_s
 /*
  * Synchronise `stream`, read the device-side flags of `workspace` and, when
  * `clear` is non-zero, reset them.  Returns LRKV_OK, LRKV_ERR_DEVICE_FAULT
- * (bad seq_len, offset or page id seen) or LRKV_ERR_TIMEOUT (a bounded wait
- * gave up).  *flags_out (if not NULL) receives the raw flag bits.
+ * (bad seq_len, row range, offset or page id seen, or a non-finite value
+ * quantised) or LRKV_ERR_TIMEOUT (a bounded wait gave up).  *flags_out (if not NULL) receives the raw flag bits.
  */
 lrkv_status lrkv_query_device_status(const void* workspace, int32_t clear, uint32_t* flags_out,
                                      lrkv_stream_t stream);
@@ -371,8 +499,8 @@ lrkv_status lrkv_query_device_status(const void* workspace, int32_t clear, uint3
 /*
  * Failure-detection test hook (no counterpart on the pages: it tests the
  * library's own error path).  Arms the next lrkv_attn_decode,
- * lrkv_attn_decode_static_scratch or lrkv_attn_prefill_chunk call made from
- * this host thread: in that launch the copy-issuing warps issue nothing and
+ * lrkv_attn_decode_static_scratch, lrkv_attn_decode_quant or
+ * lrkv_attn_prefill_chunk call made from this host thread: in that launch the copy-issuing warps issue nothing and
  * every bounded wait gives up after `spin_cap` failed attempts, so the waits
  * run out the way they would if a copy never arrived.  The launch records
  * LRKV_DEVFLAG_TIMEOUT (lrkv_query_device_status then returns

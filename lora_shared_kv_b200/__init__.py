@@ -14,6 +14,16 @@ Typical decode call::
     uv = lrkv.u_view(u)                         # u: [S, N_U, L, r] bf16
     ws = torch.zeros(lrkv.lrkv_decode_workspace_bytes(prob, L), dtype=torch.uint8, device="cuda")
     lrkv.lrkv_attn_decode(prob, q, kv, seq_lens, L, uv, b, offsets, out, ws)
+
+The base cache can be held in 8 bits (float8_e4m3fn or int8 codes, one fp32 scale
+per 64-token block and KV head)::
+
+    kv8 = lrkv.kv_view_quant_dense(k8, v8, k_scale, v_scale)   # codes [S, Hkv, L, d], scales [S, Hkv, ceil(L / 64)]
+    fws = torch.zeros(lrkv.KV_QUANT_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
+    new = lrkv.kv_view_dense(k_new, v_new)                      # [S, Hkv, 1, d] bf16, any strides
+    lrkv.lrkv_quantize_kv(prob, new, 1, kv8, L, positions, None, fws)
+    dws = torch.zeros(lrkv.lrkv_decode_quant_workspace_bytes(prob, L), dtype=torch.uint8, device="cuda")
+    lrkv.lrkv_attn_decode_quant(prob, q, kv8, seq_lens, L, uv, b, offsets, out, dws)
 """
 
 import ctypes
@@ -25,6 +35,10 @@ BASE_SHARED = 0
 BASE_LR_SHARED = 1
 BF16 = 0
 F32 = 1
+Q_E4M3 = 0
+Q_INT8 = 1
+QUANT_BLOCK = 64  # tokens of an 8-bit cache that share a scale
+KV_QUANT_WORKSPACE_BYTES = 256
 
 _STATUS = {
     0: "LRKV_OK",
@@ -52,6 +66,10 @@ EXPORTS = (
     "lrkv_query_static_scratch_status",
     "lrkv_prefill_workspace_bytes",
     "lrkv_attn_prefill_chunk",
+    "lrkv_quantize_kv",
+    "lrkv_dequantize_kv",
+    "lrkv_decode_quant_workspace_bytes",
+    "lrkv_attn_decode_quant",
     "lrkv_workspace_reset",
     "lrkv_query_device_status",
     "lrkv_debug_stall_next_launch",
@@ -89,6 +107,16 @@ class UView(ctypes.Structure):
                 ("num_rows", ctypes.c_int32)]
 
 
+class QKVView(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("stride_session", ctypes.c_int64), ("stride_head", ctypes.c_int64),
+                ("stride_token", ctypes.c_int64), ("scale_stride_session", ctypes.c_int64),
+                ("scale_stride_head", ctypes.c_int64), ("page_table", ctypes.c_void_p),
+                ("page_table_stride", ctypes.c_int64), ("stride_page", ctypes.c_int64),
+                ("scale_stride_page", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("format", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -118,6 +146,12 @@ def lib():
         L.lrkv_prefill_workspace_bytes.restype = sz
         L.lrkv_attn_prefill_chunk.argtypes = [P(Problem), vp, P(KVView), i32, i32, i32, P(UView), vp, vp, vp,
                                               i32, vp, sz, vp]
+        L.lrkv_quantize_kv.argtypes = [P(Problem), P(KVView), i32, P(QKVView), i32, vp, vp, vp, sz, vp]
+        L.lrkv_dequantize_kv.argtypes = [P(Problem), P(QKVView), i32, i32, P(KVView), vp, vp, vp, sz, vp]
+        L.lrkv_decode_quant_workspace_bytes.argtypes = [P(Problem), i32]
+        L.lrkv_decode_quant_workspace_bytes.restype = sz
+        L.lrkv_attn_decode_quant.argtypes = [P(Problem), vp, P(QKVView), vp, i32, P(UView), vp, vp, vp, i32, vp, sz,
+                                             vp]
         L.lrkv_workspace_reset.argtypes = [vp, sz, vp]
         L.lrkv_query_device_status.argtypes = [vp, i32, P(ctypes.c_uint32), vp]
         L.lrkv_query_static_scratch_status.argtypes = [i32, P(ctypes.c_uint32), vp]
@@ -129,7 +163,7 @@ def lib():
         L.lrkv_version.restype = i32
         for name in ("lrkv_append_lr_cache", "lrkv_attn_decode", "lrkv_attn_decode_kv_heads",
                      "lrkv_attn_decode_static_scratch",
-                     "lrkv_attn_prefill_chunk",
+                     "lrkv_attn_prefill_chunk", "lrkv_quantize_kv", "lrkv_dequantize_kv", "lrkv_attn_decode_quant",
                      "lrkv_workspace_reset", "lrkv_query_device_status", "lrkv_query_static_scratch_status",
                      "lrkv_debug_stall_next_launch"):
             getattr(L, name).restype = i32
@@ -188,7 +222,9 @@ def kv_view_dense(k, v):
     _require(k.dtype == torch.bfloat16 and v.dtype == torch.bfloat16 and k.dim() == 4, "k, v: bf16 [S, Hkv, L, d]")
     _require(k.stride() == v.stride() and k.stride(3) == 1, "k, v: same strides, d contiguous")
     _on_device(k=k, v=v)
-    return KVView(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2), None, 0, 0, 0, 0)
+    view = KVView(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2), None, 0, 0, 0, 0)
+    view.tensors = (k, v)  # a view keeps its tensors alive
+    return view
 
 
 def kv_view_paged(k_pages, v_pages, page_table):
@@ -198,16 +234,73 @@ def kv_view_paged(k_pages, v_pages, page_table):
     _require(page_table.dtype == torch.int32 and page_table.dim() == 2 and page_table.stride(1) == 1,
              "page_table: int32 [S, n_logical_pages], rows contiguous")
     _on_device(k_pages=k_pages, v_pages=v_pages, page_table=page_table)
-    return KVView(k_pages.data_ptr(), v_pages.data_ptr(), 0, k_pages.stride(1), k_pages.stride(2),
+    view = KVView(k_pages.data_ptr(), v_pages.data_ptr(), 0, k_pages.stride(1), k_pages.stride(2),
                   page_table.data_ptr(), page_table.stride(0), k_pages.stride(0), k_pages.shape[2],
                   k_pages.shape[0])
+    view.tensors = (k_pages, v_pages, page_table)
+    return view
+
+
+def _quant_view(k8, v8, k_scale, v_scale, what, rank):
+    fmt = {torch.float8_e4m3fn: Q_E4M3, torch.int8: Q_INT8}.get(k8.dtype)
+    _require(fmt is not None and v8.dtype == k8.dtype and k8.dim() == 4 and k8.shape == v8.shape,
+             f"k8, v8: float8_e4m3fn or int8 {what}, same shape")
+    _require(k8.stride() == v8.stride() and k8.stride(3) == 1, "k8, v8: same strides, d contiguous")
+    _require(k_scale.dtype == torch.float32 and v_scale.dtype == torch.float32 and k_scale.dim() == rank
+             and k_scale.shape == v_scale.shape and k_scale.stride() == v_scale.stride(),
+             "k_scale, v_scale: fp32, same shape and strides")
+    _on_device(k8=k8, v8=v8, k_scale=k_scale, v_scale=v_scale)
+    view = QKVView(k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr())
+    view.format = fmt
+    view.stride_head, view.stride_token = k8.stride(1), k8.stride(2)
+    view.scale_stride_head = k_scale.stride(1)
+    view.tensors = (k8, v8, k_scale, v_scale)
+    return view
+
+
+def kv_view_quant_dense(k8, v8, k_scale, v_scale):
+    """k8, v8: float8_e4m3fn or int8 codes [S, Hkv, L, d] with d contiguous; k_scale, v_scale: fp32
+    [S, Hkv, >= ceil(L / 64)], one scale per block of 64 tokens, blocks contiguous."""
+    view = _quant_view(k8, v8, k_scale, v_scale, "[S, Hkv, L, d]", 3)
+    blocks = -(-k8.shape[2] // QUANT_BLOCK)
+    _require(k_scale.shape[:2] == k8.shape[:2] and k_scale.shape[2] >= blocks and k_scale.stride(2) == 1,
+             f"scales: [S, Hkv, >= {blocks}] with the blocks contiguous")
+    view.stride_session, view.scale_stride_session = k8.stride(0), k_scale.stride(0)
+    view.holds = (k8.shape[0], k8.shape[1], k8.shape[2], k8.shape[3])
+    return view
+
+
+def kv_view_quant_paged(k8_pages, v8_pages, k_scale, v_scale, page_table):
+    """k8_pages, v8_pages: codes [P, Hkv, 64, d]; k_scale, v_scale: fp32 [P, Hkv]; page_table: int32
+    [S, n_logical_pages] on the device."""
+    view = _quant_view(k8_pages, v8_pages, k_scale, v_scale, "[P, Hkv, 64, d]", 2)
+    _require(k_scale.shape == k8_pages.shape[:2], "scales: one per page and KV head, [P, Hkv]")
+    _require(page_table.dtype == torch.int32 and page_table.dim() == 2 and page_table.stride(1) == 1,
+             "page_table: int32 [S, n_logical_pages], rows contiguous")
+    _on_device(page_table=page_table)
+    view.page_table, view.page_table_stride = page_table.data_ptr(), page_table.stride(0)
+    view.stride_page, view.scale_stride_page = k8_pages.stride(0), k_scale.stride(0)
+    view.page_size, view.num_pages = k8_pages.shape[2], k8_pages.shape[0]
+    view.tensors += (page_table,)
+    view.holds = (page_table.shape[0], k8_pages.shape[1], page_table.shape[1] * QUANT_BLOCK, k8_pages.shape[3])
+    return view
+
+
+def _quant_fits(view, problem, rows):
+    """The view's buffers hold the problem's sessions, KV heads and head_dim, and `rows` rows of each."""
+    need = (problem.num_sessions, problem.num_kv_heads, int(rows), problem.head_dim)
+    _require(all(h >= n for h, n in zip(view.holds, need)) and view.holds[3] == need[3],
+             f"the 8-bit view holds [sessions, KV heads, rows, head_dim] {view.holds}, the call needs {need}")
+    _on_device(**{f"8-bit view tensor {i}": t for i, t in enumerate(view.tensors)})
 
 
 def u_view(u):
     """u: bf16 [S, N_U, rows, r] with r contiguous."""
     _require(u.dtype == torch.bfloat16 and u.dim() == 4 and u.stride(3) == 1, "u: bf16 [S, N_U, rows, r], r contiguous")
     _on_device(u=u)
-    return UView(u.data_ptr(), u.stride(0), u.stride(1), u.stride(2), u.shape[2])
+    view = UView(u.data_ptr(), u.stride(0), u.stride(1), u.stride(2), u.shape[2])
+    view.tensors = (u,)
+    return view
 
 
 # ---------------------------------------------------------------------------
@@ -321,6 +414,66 @@ def lrkv_attn_prefill_chunk(problem, q, kv, session, ctx_len, T, u, b, offsets, 
     _check(lib().lrkv_attn_prefill_chunk(ctypes.byref(problem), _ptr(q), ctypes.byref(kv), int(session),
                                          int(ctx_len), int(T), ctypes.byref(uv), _ptr(b), _ptr(offsets),
                                          _ptr(out), odt, _ptr(workspace), nbytes, _stream(stream)))
+
+
+def _row_ranges(problem, first_rows, row_counts, workspace):
+    for name, t in (("first_rows", first_rows), ("row_counts", row_counts)):
+        if t is not None:
+            _require(t.dtype == torch.int32 and t.is_contiguous() and t.numel() >= problem.num_sessions,
+                     f"{name}: int32 [num_sessions], contiguous")
+    _on_device(first_rows=first_rows, row_counts=row_counts, workspace=workspace)
+
+
+def lrkv_quantize_kv(problem, src, T, dst, dst_rows, first_rows, row_counts, workspace, stream=None):
+    """Write rows [0, n) of every session of the bf16 view `src` into rows [f, f + n) of the 8-bit view `dst`, which
+    holds dst_rows rows a session: f = first_rows[s] (0 when None), n = row_counts[s] (T when None).  The cache then
+    holds f + n tokens of the session."""
+    _row_ranges(problem, first_rows, row_counts, workspace)
+    _quant_fits(dst, problem, dst_rows)
+    _check(lib().lrkv_quantize_kv(ctypes.byref(problem), ctypes.byref(src), int(T), ctypes.byref(dst), int(dst_rows),
+                                  _ptr(first_rows), _ptr(row_counts), _ptr(workspace),
+                                  workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def lrkv_dequantize_kv(problem, src, src_rows, T, dst, first_rows, row_counts, workspace, stream=None):
+    """Read rows [f, f + n) of every session of the 8-bit view `src` (src_rows rows a session) back into rows [0, n)
+    of the bf16 view `dst`; f, n and T as in lrkv_quantize_kv."""
+    _row_ranges(problem, first_rows, row_counts, workspace)
+    _quant_fits(src, problem, src_rows)
+    _check(lib().lrkv_dequantize_kv(ctypes.byref(problem), ctypes.byref(src), int(src_rows), int(T),
+                                    ctypes.byref(dst), _ptr(first_rows), _ptr(row_counts), _ptr(workspace),
+                                    workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def lrkv_decode_quant_workspace_bytes(problem, max_seq_len):
+    n = lib().lrkv_decode_quant_workspace_bytes(ctypes.byref(problem), int(max_seq_len))
+    if n == 0:
+        raise LrkvError(1, "invalid decode shape")
+    return n
+
+
+def lrkv_attn_decode_quant(problem, q, kv, seq_lens, max_seq_len, u, b, offsets, out, workspace, stream=None):
+    """lrkv_attn_decode over an 8-bit base cache (kv: a kv_view_quant_dense or kv_view_quant_paged view)."""
+    _require(q.is_contiguous() and b.is_contiguous() and out.is_contiguous(), "q, b and out must be contiguous")
+    _require(q.dtype == torch.bfloat16 and b.dtype == torch.bfloat16, "q and b: bf16")
+    _require(out.dtype in (torch.bfloat16, torch.float32), "out: bf16 or fp32")
+    _require(seq_lens.dtype == torch.int32 and seq_lens.is_contiguous() and seq_lens.numel() >= problem.num_sessions,
+             "seq_lens: int32 [num_sessions], contiguous")
+    rows = problem.num_sessions * problem.num_agents
+    _require(offsets is None or (offsets.dtype == torch.int32 and offsets.is_contiguous() and offsets.numel() >= rows),
+             "offsets: int32 [num_sessions, num_agents], contiguous, or None")
+    size = rows * problem.num_q_heads * problem.head_dim
+    _require(q.numel() >= size and out.numel() >= size, "q and out: [num_sessions, num_agents, num_q_heads, head_dim]")
+    _require(b.numel() >= problem.num_agents * problem.rank * problem.num_kv_heads * problem.head_dim,
+             "b: [num_agents, rank, num_kv_heads * head_dim]")
+    _on_device(q=q, seq_lens=seq_lens, b=b, offsets=offsets, out=out, workspace=workspace)
+    _quant_fits(kv, problem, max_seq_len)
+    odt = F32 if out.dtype == torch.float32 else BF16
+    uv = u if isinstance(u, UView) else u_view(u)
+    _check(lib().lrkv_attn_decode_quant(ctypes.byref(problem), _ptr(q), ctypes.byref(kv), _ptr(seq_lens),
+                                        int(max_seq_len), ctypes.byref(uv), _ptr(b), _ptr(offsets), _ptr(out), odt,
+                                        _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                        _stream(stream)))
 
 
 def lrkv_workspace_reset(workspace, stream=None):

@@ -1,0 +1,1081 @@
+// Decode attention over a shared base K/V cache held in 8 bits, with per-agent
+// low-rank value caches in bf16.
+//
+// For every (session s, agent i, query head h), with g = h / G and codes c and
+// block scales s of the cache,
+//     o = ( sum_t p_t sv c_v[t]  +  (p Umask_i) B_i,g ) / l
+//     p_t = exp2(sk (q . c_k[t]) scale log2e - m)
+// the same reordered form as over a bf16 cache: the rank-r product is accumulated
+// per row and B_i applied once.
+//
+//  * What bounds it: the codes are read once from HBM, 2 d bytes a key and head,
+//    half a bf16 cache's.  At that rate an SM gets a 64-key tile (16 KB at d =
+//    128) every 730 cycles, and has to turn its 16 K codes into fp16 (the tensor
+//    cores' fp8 form is no faster for warp-level MMAs here, and would round q
+//    and p to 4 bits): a conversion per two codes at half rate, 128 cycles, and
+//    per 16 rows 128 MMAs of m16n8k16 at 2 cycles, 256 cycles.
+//  * A warp holds ALL rows of its row block (8, 16 or 16 + 8) and a slice of the
+//    tile's keys, so that a code is converted once per tile.  The 16-row part
+//    has rows as the MMA's M, the 8-row part has keys (or dims) as M; the
+//    converted registers of K and V serve both as they are:
+//      K (two 8-key fragments of 4 dims a lane) is B of S = Q K^T and A of S^T = K Q^T;
+//      V (from ldmatrix's transposing byte form) is B of O += P V and A of O^T += V^T P^T.
+//  * Key order inside 16 keys: MMA slot s is key s ^ ((s & 8) >> 1).  V's rows come
+//    four consecutive per lane, slots (2t, 2t+1, 2t+8, 2t+9); with this order the
+//    eight rows of every ldmatrix phase, K's and V's, lie in different 16-byte
+//    banks of the swizzled tile.
+//  * Softmax: running reference m per row, moved only when a tile beats it by 2^8.
+//    The weights enter the value product as fp16, times the block's value scale:
+//    p' = p 2^(m - w) sv, with a second reference w per row that keeps the largest
+//    p' between 2^8 and 2^15 (fp16 ends at 2^16 and is full-precision down to
+//    2^-14).  So p' carries 11 bits down to 2^-22 of the largest weight and 2^-33
+//    absolute, whatever the scales.  The low-rank product takes p as bf16.
+//  * The flattened (item, tile) space of the actual lengths is split evenly over
+//    the CTAs (each counts the sessions' tiles at its start), so ragged batches
+//    are balanced; an item cut between CTAs is merged by the last one to finish.
+//  * Keys past seq_len and U rows before a_i are removed by selects on operands.
+#pragma once
+
+#include <float.h>
+#include <math.h>
+
+#include "common.cuh"
+#include "quant.h"
+#include "quant_device.cuh"
+
+namespace lrkv {
+
+namespace {
+
+constexpr float kNegInf = -INFINITY;
+constexpr int kMergeBatch = 4;  // partial records whose loads are in flight together
+
+// The CTA's share of the work, found by warp 0.
+struct Range {
+  long long W, t_begin, t_end;  // tiles of the launch; this CTA's
+  long long base;               // first tile of session s
+  int s;                        // session of t_begin
+  int ctas;                     // CTAs that take part
+  int whole;                    // whole items, one per CTA
+  int pad;
+};
+
+// Stage facts that do not come through the tile copies.
+struct Meta {
+  float ks, vs;
+  int ok, pad;
+};
+
+__device__ __forceinline__ int clamp_len(const QDecodeParams& p, int sl) {
+  sl = sl < 0 ? 0 : sl;
+  sl = sl > p.max_seq_len ? p.max_seq_len : sl;
+  return sl > p.u_rows ? p.u_rows : sl;
+}
+__device__ __forceinline__ int session_len(const QDecodeParams& p, int s) { return clamp_len(p, __ldg(p.seq_lens + s)); }
+// An empty session keeps one (empty) tile per item, so that its rows are written.
+__device__ __forceinline__ int tiles_of(int sl) { return sl > 0 ? (sl + kQBlock - 1) / kQBlock : 1; }
+
+// Warp 0: count every session's tiles, then find this CTA's range.
+__device__ __forceinline__ void find_range(const QDecodeParams& p, Range* out) {
+  const int lane = threadIdx.x & 31;
+  const int HR = p.Hkv * p.n_rg;
+  long long total = 0;
+  int nt_max = 0;
+  bool bad = false;
+  for (int s0 = 0; s0 < p.S; s0 += 32) {
+    const int s = s0 + lane;
+    int nt = 0;
+    if (s < p.S) {
+      const int sl = __ldg(p.seq_lens + s);
+      bad |= sl != clamp_len(p, sl);
+      nt = tiles_of(clamp_len(p, sl));
+    }
+    total += nt;
+    nt_max = max(nt_max, nt);
+  }
+  if (blockIdx.x == 0 && __any_sync(0xFFFFFFFFu, bad) && lane == 0) atomicOr(p.flags, LRKV_DEVFLAG_SEQLEN);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+  nt_max = __reduce_max_sync(0xFFFFFFFFu, nt_max);
+  const long long W = total * HR;
+  const long long items = (long long)p.S * HR;
+  const int C = (int)(W < (long long)gridDim.x ? W : (long long)gridDim.x);
+  const bool whole = q_whole_items(items, C, nt_max, W, p.whole_slack);
+  const int c = blockIdx.x;
+  const int ctas = whole ? (int)items : C;
+  Range r = {};
+  r.W = W;
+  r.ctas = ctas;
+  r.whole = whole;
+  if (c < ctas) {
+    long long t0 = whole ? 0 : c * W / ctas;
+    r.t_end = whole ? 0 : (c + 1) * W / ctas;
+    const int s_whole = c / HR;
+    // the session that holds the first tile (or item), and its first tile
+    long long base = 0;
+    for (int s0 = 0; s0 < p.S; s0 += 32) {
+      const int s = s0 + lane;
+      const int nt = s < p.S ? tiles_of(session_len(p, s)) : 0;
+      int incl = nt;  // at most 32 sessions of 2^25 tiles
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= o) incl += up;
+      }
+      const long long mine = base + (long long)(incl - nt) * HR;
+      const bool here = s < p.S && (whole ? s == s_whole : (t0 >= mine && t0 < mine + (long long)nt * HR));
+      const unsigned hit = __ballot_sync(0xFFFFFFFFu, here);
+      if (hit) {
+        const int src = __ffs(hit) - 1;
+        r.s = s0 + src;
+        r.base = __shfl_sync(0xFFFFFFFFu, mine, src);
+        if (whole) {
+          const int n = __shfl_sync(0xFFFFFFFFu, nt, src);
+          t0 = r.base + (long long)(c % HR) * n;
+          r.t_end = t0 + n;
+        }
+        break;
+      }
+      base += (long long)__shfl_sync(0xFFFFFFFFu, incl, 31) * HR;
+    }
+    r.t_begin = t0;
+  }
+  if (lane == 0) *out = r;
+}
+
+// One CTA's stretch of one item.
+struct Seg {
+  int item, s, g, rg;
+  int lo, hi;            // its tiles [lo, hi) of the item's nt
+  int sl;                // session length
+  long long item_t0;     // the item's first tile
+  int nt;
+  int row_lo, rows;      // query rows [row_lo, row_lo + rows) of the N*G rows of this KV head
+  int i_lo, n_ag;        // agents spanned by them
+};
+
+// Walks a CTA's range segment by segment; every role does so alike.
+struct Walk {
+  long long t, t_end, base;
+  int s, nt, sl;
+  __device__ __forceinline__ void start(const QDecodeParams& p, const Range& r) {
+    t = r.t_begin;
+    t_end = r.t_end;
+    base = r.base;
+    s = r.s;
+    sl = t < t_end ? session_len(p, s) : 0;
+    nt = tiles_of(sl);
+  }
+  __device__ __forceinline__ bool next(const QDecodeParams& p, Seg& sg) {
+    if (t >= t_end) return false;
+    const int HR = p.Hkv * p.n_rg;
+    while (t >= base + (long long)nt * HR) {
+      base += (long long)nt * HR;
+      sl = session_len(p, ++s);
+      nt = tiles_of(sl);
+    }
+    const int in = (int)(t - base);  // < nt * HR, checked on the host to fit
+    const int idx = in / nt;
+    sg.lo = in - idx * nt;
+    const long long left = t_end - t;
+    sg.hi = left < nt - sg.lo ? sg.lo + (int)left : nt;
+    sg.s = s;
+    sg.sl = sl;
+    sg.nt = nt;
+    sg.item = s * HR + idx;
+    sg.item_t0 = base + (long long)idx * nt;
+    sg.g = idx / p.n_rg;
+    sg.rg = idx - sg.g * p.n_rg;
+    sg.row_lo = sg.rg * p.rows_per_group;
+    const int row_hi = min(sg.row_lo + p.rows_per_group, p.rows_total);
+    sg.rows = row_hi - sg.row_lo;
+    sg.i_lo = sg.row_lo / p.G;
+    sg.n_ag = (row_hi - 1) / p.G - sg.i_lo + 1;
+    t += sg.hi - sg.lo;
+    return true;
+  }
+};
+
+__device__ __forceinline__ int load_offset(const QDecodeParams& p, int s, int agent, bool flag_errors) {
+  if (p.offsets == nullptr) return 0;
+  int a = __ldg(p.offsets + (size_t)s * p.N + agent);
+  if (a < 0) {
+    if (flag_errors) atomicOr(p.flags, LRKV_DEVFLAG_OFFSET);
+    a = 0;
+  }
+  return a;
+}
+
+// ---------------------------------------------------------------------------
+// producer warp
+// ---------------------------------------------------------------------------
+// Tile n of the CTA goes to ring stage n % stages.  A stage is full after two
+// arrivals: the bytes of the tile copies, and the two scales' 4-byte copies.
+template <int D, int RK>
+__device__ void q_producer(const QDecodeParams& p, const CUtensorMap* tmK, const CUtensorMap* tmV,
+                           const CUtensorMap* tmU, uint8_t* ring, const QDecodeSmem& lay, Meta* meta, uint64_t* full,
+                           uint64_t* empty, volatile int* abort_flag, const Range& range) {
+  const int lane = threadIdx.x & 31;
+  const uint64_t pol_kv = policy_evict_first();
+  const uint64_t pol_u = policy_evict_last();
+  constexpr int KV_BYTES = kQBlock * D;
+  constexpr int U_BYTES = kQBlock * RK * 2;
+  const bool paged = p.page_table != nullptr;
+  int stage = 0, n = 0;
+  uint32_t phase = 0;
+  bool stop = p.stall != 0;  // the test hook: issue nothing, so the consumers' waits run out
+  Walk walk;
+  walk.start(p, range);
+  Seg sg;
+  while (!stop && walk.next(p, sg)) {
+    if (sg.sl == 0) continue;
+    const int my_a = lane < sg.n_ag ? load_offset(p, sg.s, sg.i_lo + lane, false) : 0x7fffffff;
+    int ids = 0;
+    for (int tile = sg.lo; tile < sg.hi; ++tile) {
+      const int k = tile - sg.lo;
+      if (paged && (k & 31) == 0)  // page ids of the next 32 tiles, one per lane
+        ids = tile + lane < sg.hi ? __ldg(p.page_table + (size_t)sg.s * p.pt_stride + tile + lane) : 0;
+      const int page = paged ? __shfl_sync(0xFFFFFFFFu, ids, k & 31) : 0;
+      const unsigned need = __ballot_sync(0xFFFFFFFFu, lane < sg.n_ag && (tile + 1) * kQBlock > my_a);
+      const bool ok = !paged || (page >= 0 && page < p.num_pages);
+      const unsigned umask = !ok ? 0u : p.mode == LRKV_BASE_SHARED ? need : (need ? 1u : 0u);
+      const bool freed = mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, p.flags, p.spin_cap, true);
+      // After an abort the consumers release stages without waiting for their
+      // copies, so nothing more may be issued; the whole warp leaves together.
+      if (__any_sync(0xFFFFFFFFu, !freed || *abort_flag)) {
+        stop = true;
+        break;
+      }
+      if (lane == 0) {
+        uint8_t* st = ring + (size_t)stage * lay.stage_bytes;
+        meta[stage].ok = ok;
+        if (!ok) {
+          atomicOr(p.flags, LRKV_DEVFLAG_PAGE);
+          mbar_arrive(&full[stage]);
+          mbar_arrive(&full[stage]);
+        } else {
+          const long long sc = paged ? page * p.s_sp + sg.g * p.s_sh : sg.s * p.s_ss + sg.g * p.s_sh + tile;
+          mbar_arrive_expect_tx(&full[stage], 2 * KV_BYTES + __popc(umask) * U_BYTES);
+          const int c1 = paged ? 0 : tile * kQBlock;
+          const int c3 = paged ? page : sg.s;
+          tma_load_4d(st, tmK, &full[stage], 0, c1, sg.g, c3, pol_kv);
+          tma_load_4d(st + KV_BYTES, tmV, &full[stage], 0, c1, sg.g, c3, pol_kv);
+          cp_async4(smem_u32(&meta[stage].ks), p.k_scale + sc);
+          cp_async4(smem_u32(&meta[stage].vs), p.v_scale + sc);
+          cp_async_mbar_arrive(&full[stage]);
+          unsigned m = umask;
+          while (m) {
+            const int slot = __ffs(m) - 1;
+            m &= m - 1;
+            tma_load_4d(st + 2 * KV_BYTES + slot * U_BYTES, tmU, &full[stage], 0, tile * kQBlock,
+                        p.mode == LRKV_BASE_SHARED ? sg.i_lo + slot : 0, sg.s, pol_u);
+          }
+        }
+      }
+      __syncwarp();
+      ++n;
+      if (++stage == p.stages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+  }
+  // After an abort the consumers may stop waiting; no copy of this CTA may still
+  // be landing in shared memory when it exits.
+  if (lane == 0) {
+    cp_async_wait<0>();
+    if (*abort_flag) {
+      const int m = n < p.stages ? n : p.stages;
+      int st = stage;
+      uint32_t ph = phase;
+      for (int j = 0; j < m; ++j) {
+        if (--st < 0) {
+          st = p.stages - 1;
+          ph ^= 1;
+        }
+        uint32_t spins = 0;
+        while (!mbar_try_wait(&full[st], ph) && ++spins < kSpinCap) {
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// consumer warps
+// ---------------------------------------------------------------------------
+template <int D, int RK, int H16, int H8>
+struct WarpRows {
+  static constexpr int RPW = 16 * H16 + 8 * H8;  // rows of a row block
+  static constexpr int KS = D / 16;
+  static constexpr int MZ = RK >= 16 ? RK / 16 : 1;
+  // 16-row part: this lane's rows are g8 and g8 + 8.  8-row part (rows 16 H16 ..):
+  // rows 2 t4 and 2 t4 + 1.  Index 0, 1: the first; 2, 3: the second part's.
+  static constexpr int NR = 2 * (H16 + H8);
+  static constexpr int R8 = 2 * H16;             // first index of the 8-row part
+  uint32_t q16[H16 ? KS : 1][4];
+  uint32_t q8[H8 ? KS : 1][2];
+  float c[NR];      // what turns a row's raw score into log2 units, without the block's key scale
+  float m[NR];      // softmax reference (log2 units) of l and Z
+  float w[NR];      // reference of O
+  float l[NR];      // this lane's part of the row sum
+  float o16[H16 ? D / 8 : 1][4];
+  float z16[H16 ? RK / 8 : 1][4];
+  float o8[H8 ? D / 16 : 1][4];
+  float z8[H8 ? MZ : 1][4];
+};
+
+// Power of two that brings a row's largest |q| into [2^14, 2^15) (fp16 then holds
+// every bf16 element down to 2^-28 of it exactly), and its inverse.
+__device__ __forceinline__ void row_factor(float amax, float& f, float& inv) {
+  int e = (int)(__float_as_uint(amax) >> 23) - 127;
+  e = amax > 0.f && e < 128 ? min(14 - e, 113) : 0;  // at least 14 - 127 = -113
+  f = __uint_as_float((uint32_t)(e + 127) << 23);
+  inv = __uint_as_float((uint32_t)(127 - e) << 23);
+}
+
+__device__ __forceinline__ float bf_lo(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
+
+__device__ __forceinline__ const __nv_bfloat16* q_row(const QDecodeParams& p, const Seg& sg, int D, int row) {
+  const int grow = sg.row_lo + row;
+  return static_cast<const __nv_bfloat16*>(p.q) +
+         (((size_t)sg.s * p.N + grow / p.G) * p.Hq + (size_t)sg.g * p.G + grow % p.G) * D;
+}
+
+// The row block's queries as fp16 fragments.  A lane's four dims of a 16-dim step
+// are 4 t4 .. + 3 (the bytes that ldmatrix gives it of K).
+template <int D, int RK, int H16, int H8>
+__device__ __forceinline__ void load_queries(const QDecodeParams& p, const Seg& sg, int rbase,
+                                             WarpRows<D, RK, H16, H8>& st) {
+  constexpr int KS = D / 16;
+  const int lane = threadIdx.x & 31, g8 = lane >> 2, t4 = lane & 3;
+  constexpr int PARTS = 2 * H16 + H8;  // rows whose elements this lane holds
+  uint2 raw[PARTS][KS];
+  float f[PARTS], inv[PARTS];
+#pragma unroll
+  for (int i = 0; i < PARTS; ++i) {
+    const int row = rbase + 8 * i + g8;
+    const bool live = row < sg.rows;
+    const __nv_bfloat16* src = live ? q_row(p, sg, D, row) : nullptr;
+    float amax = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      raw[i][ks] = live ? __ldg(reinterpret_cast<const uint2*>(src + 16 * ks + 4 * t4)) : make_uint2(0, 0);
+    }
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
+      amax = fmaxf(amax, fmaxf(fmaxf(fabsf(bf_lo(raw[i][ks].x)), fabsf(bf_hi(raw[i][ks].x))),
+                               fmaxf(fabsf(bf_lo(raw[i][ks].y)), fabsf(bf_hi(raw[i][ks].y)))));
+    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+    row_factor(amax, f[i], inv[i]);
+  }
+#pragma unroll
+  for (int ks = 0; ks < KS; ++ks) {
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i) {
+      const uint32_t lo = pack_f16x2(bf_lo(raw[i][ks].x) * f[i], bf_hi(raw[i][ks].x) * f[i]);
+      const uint32_t hi = pack_f16x2(bf_lo(raw[i][ks].y) * f[i], bf_hi(raw[i][ks].y) * f[i]);
+      if (H16 && i < 2) {
+        st.q16[ks][i] = lo;
+        st.q16[ks][i + 2] = hi;
+      } else {
+        st.q8[ks][0] = lo;
+        st.q8[ks][1] = hi;
+      }
+    }
+  }
+  if constexpr (H16) {
+    st.c[0] = inv[0] * p.scale_log2;
+    st.c[1] = inv[1] * p.scale_log2;
+  }
+  if constexpr (H8) {  // rows 2 t4, 2 t4 + 1 belong to the lanes with g8 = 2 t4, 2 t4 + 1
+    const float mine = inv[PARTS - 1] * p.scale_log2;
+    st.c[2 * H16] = __shfl_sync(0xFFFFFFFFu, mine, 8 * t4);
+    st.c[2 * H16 + 1] = __shfl_sync(0xFFFFFFFFu, mine, 8 * t4 + 4);
+  }
+}
+
+// Byte offset of 16-byte chunk c of key k in a swizzled tile (128-byte swizzle at
+// d = 128, 64-byte at d = 64).
+template <int D>
+__device__ __forceinline__ uint32_t tile_at(int k, int c) {
+  return D == 128 ? k * 128 + ((c ^ (k & 7)) << 4) : k * 64 + ((c ^ ((k >> 1) & 3)) << 4);
+}
+// Same for a U tile (rows of 2 RK bytes: no swizzle, 32-byte, 64-byte).
+template <int RK>
+__device__ __forceinline__ uint32_t u_at(int k, int c) {
+  return RK == 8 ? k * 16 : RK == 16 ? k * 32 + ((c ^ ((k >> 2) & 1)) << 4) : k * 64 + ((c ^ ((k >> 1) & 3)) << 4);
+}
+
+__device__ __forceinline__ int slot_key(int s) { return s ^ ((s & 8) >> 1); }
+
+// One warp's KPW keys (from key kw of the tile on) of one tile.
+template <int FMT, int D, int RK, int H16, int H8, int KPW>
+__device__ __forceinline__ void q_tile(const QDecodeParams& p, WarpRows<D, RK, H16, H8>& st, const Seg& sg,
+                                       uint32_t Ks, const Meta& mt, int key0, int kw, const int* a_sm, int ag_lo,
+                                       int ag_hi, const int* my_ag, int a_first, int a_max) {
+  using WR = WarpRows<D, RK, H16, H8>;
+  constexpr int KS = D / 16;
+  constexpr int NB = KPW / 16;  // blocks of 16 keys
+  constexpr int NR = WR::NR;
+  constexpr int R8 = WR::R8;
+  const int lane = threadIdx.x & 31, g8 = lane >> 2, t4 = lane & 3;
+  const uint32_t Vs = Ks + kQBlock * D;
+  const uint32_t Us = Vs + kQBlock * D;
+  const int sl = sg.sl;
+
+  // ---- scores: S = Q K^T (16-row part), S^T = K Q^T (8-row part)
+  float s16[H16 ? NB : 1][2][4], s8[H8 ? NB : 1][4];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (H16) s16[nb][0][e] = s16[nb][1][e] = 0.f;
+      if constexpr (H8) s8[nb][e] = 0.f;
+    }
+  {
+    const int j = lane >> 3, key = kw + slot_key((j & 1) * 8 + (lane & 7));
+#pragma unroll
+    for (int cc = 0; cc < KS / 2; ++cc) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        uint32_t r[4];  // chunk 2cc: slots 0-7, 8-15; chunk 2cc + 1 likewise
+        ldsm_x4(r[0], r[1], r[2], r[3], Ks + tile_at<D>(key + 16 * nb, 2 * cc + (j >> 1)));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t a0, a2, b0, b2;
+          codes_to_half2<FMT>(r[2 * h], a0, a2);
+          codes_to_half2<FMT>(r[2 * h + 1], b0, b2);
+          const int ks = 2 * cc + h;
+          if constexpr (H16) {
+            mma_f16_16816(s16[nb][0], st.q16[ks][0], st.q16[ks][1], st.q16[ks][2], st.q16[ks][3], a0, a2);
+            mma_f16_16816(s16[nb][1], st.q16[ks][0], st.q16[ks][1], st.q16[ks][2], st.q16[ks][3], b0, b2);
+          }
+          if constexpr (H8) mma_f16_16816(s8[nb], a0, b0, a2, b2, st.q8[ks][0], st.q8[ks][1]);
+        }
+      }
+    }
+  }
+
+  // ---- softmax
+  const bool boundary = key0 + kQBlock > sl;
+  const int k_lo = key0 + kw + 2 * t4;                 // keys of slots 2 t4 (+ 1)
+  const int k_hi = key0 + kw + 8 + ((2 * t4) ^ 4);     // keys of slots 2 t4 + 8 (+ 9)
+  if (boundary) {  // keys at or past seq_len are selected out
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      if constexpr (H16) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s16[nb][0][e] = k_lo + 16 * nb + (e & 1) < sl ? s16[nb][0][e] : kNegInf;
+          s16[nb][1][e] = k_hi + 16 * nb + (e & 1) < sl ? s16[nb][1][e] : kNegInf;
+        }
+      }
+      if constexpr (H8) {
+        const int ka = key0 + kw + 16 * nb + g8, kb = key0 + kw + 16 * nb + 8 + (g8 ^ 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s8[nb][e] = (e < 2 ? ka : kb) < sl ? s8[nb][e] : kNegInf;
+      }
+    }
+  }
+  float sc[NR], mx[NR];
+#pragma unroll
+  for (int i = 0; i < NR; ++i) {
+    sc[i] = st.c[i] * mt.ks;
+    mx[i] = kNegInf;
+  }
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    if constexpr (H16) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        mx[i] = fmaxf(mx[i], fmaxf(fmaxf(s16[nb][0][2 * i], s16[nb][0][2 * i + 1]),
+                                   fmaxf(s16[nb][1][2 * i], s16[nb][1][2 * i + 1])));
+    }
+    if constexpr (H8) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) mx[R8 + i] = fmaxf(mx[R8 + i], fmaxf(s8[nb][i], s8[nb][2 + i]));
+    }
+  }
+  // The scale is >= 0 and rounding monotonic: the scaled maximum is the maximum of
+  // the scaled scores.  Each lane checks its own keys; the lanes of a row agree on
+  // a new reference only on the few tiles that need one.
+  const float lvs = __log2f(mt.vs);
+  bool need = false;
+#pragma unroll
+  for (int i = 0; i < NR; ++i) {
+    mx[i] *= sc[i];
+    need |= mx[i] > fminf(st.m[i] + 8.f, st.w[i] + 15.f - lvs);
+  }
+  if (__any_sync(0xFFFFFFFFu, need)) {
+    float al[NR], be[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      const int lo = i < R8 ? 1 : 4, hi = i < R8 ? 2 : 16;  // lanes that share the row
+#pragma unroll
+      for (int o = lo; o <= hi; o <<= 1) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xFFFFFFFFu, mx[i], o));
+      const float mn = fmaxf(st.m[i], mx[i]);
+      al[i] = mn == kNegInf ? 1.f : fast_exp2(st.m[i] - mn);
+      st.m[i] = mn;
+      const float top = mx[i] + lvs;
+      const float wn = top > st.w[i] + 15.f ? top - 8.f : st.w[i];
+      be[i] = wn == kNegInf ? 1.f : fast_exp2(st.w[i] - wn);
+      st.w[i] = wn;
+      st.l[i] *= al[i];
+    }
+    if constexpr (H16) {
+#pragma unroll
+      for (int x = 0; x < D / 8; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st.o16[x][e] *= be[e >> 1];
+#pragma unroll
+      for (int x = 0; x < RK / 8; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st.z16[x][e] *= al[e >> 1];
+    }
+    if constexpr (H8) {
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st.o8[x][e] *= be[R8 + (e & 1)];
+#pragma unroll
+      for (int x = 0; x < WR::MZ; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st.z8[x][e] *= al[R8 + (e & 1)];
+    }
+  }
+  float mu[NR], f[NR];
+#pragma unroll
+  for (int i = 0; i < NR; ++i) {
+    mu[i] = st.m[i] == kNegInf ? 0.f : st.m[i];
+    f[i] = fast_exp2(mu[i] - (st.w[i] == kNegInf ? 0.f : st.w[i]) + lvs);  // 2^(m - w) sv
+  }
+  // weights: pz (bf16) for the low-rank product, pv (fp16, scaled) for the values
+  uint32_t pv16[H16 ? NB : 1][4], pz16[H16 ? NB : 1][4], pv8[H8 ? NB : 1][2], pz8[H8 ? NB : 1][2];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    if constexpr (H16) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {  // A fragment: rows g8, g8 + 8 of slots 2 t4 + 8 x (+ 1)
+          const float p0 = fast_exp2(fmaf(s16[nb][x][2 * i], sc[i], -mu[i]));
+          const float p1 = fast_exp2(fmaf(s16[nb][x][2 * i + 1], sc[i], -mu[i]));
+          st.l[i] += p0 + p1;
+          pz16[nb][2 * x + i] = pack_bf16x2(p0, p1);
+          pv16[nb][2 * x + i] = pack_f16x2(p0 * f[i], p1 * f[i]);
+        }
+    }
+    if constexpr (H8) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {  // S^T: slots g8 + 8 x, rows 2 t4, + 1; transposed into a B fragment
+        const float p0 = fast_exp2(fmaf(s8[nb][2 * x], sc[R8], -mu[R8]));
+        const float p1 = fast_exp2(fmaf(s8[nb][2 * x + 1], sc[R8 + 1], -mu[R8 + 1]));
+        st.l[R8] += p0;
+        st.l[R8 + 1] += p1;
+        pz8[nb][x] = movmatrix_t(pack_bf16x2(p0, p1));
+        pv8[nb][x] = movmatrix_t(pack_f16x2(p0 * f[R8], p1 * f[R8 + 1]));
+      }
+    }
+  }
+
+  // ---- values: O += P V, O^T += V^T P^T
+  {
+    const int e = lane & 15;  // row of a 16 x 16 block: slots 2t, 2t + 1, 2t + 8, 2t + 9 for rows 4t ..
+    const int key = kw + slot_key(2 * (e >> 2) + (e & 1) + 8 * ((e >> 1) & 1));
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      uint32_t vm = 0xFFFFFFFFu;  // a lane's four codes belong to four keys
+      if (boundary)
+        vm = (k_lo + 16 * nb < sl ? 0xFFu : 0u) | (k_lo + 16 * nb + 1 < sl ? 0xFF00u : 0u) |
+             (k_hi + 16 * nb < sl ? 0xFF0000u : 0u) | (k_hi + 16 * nb + 1 < sl ? 0xFF000000u : 0u);
+#pragma unroll
+      for (int cc = 0; cc < KS / 2; ++cc) {
+        uint32_t r[4];  // dims 32 cc + 8 x + g8
+        ldsm_b8_x2_t(r[0], r[1], r[2], r[3], Vs + tile_at<D>(key + 16 * nb, 2 * cc + (lane >> 4)));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t a0, a1, b0, b1;
+          codes_to_half2<FMT>(r[2 * h] & vm, a0, a1);
+          codes_to_half2<FMT>(r[2 * h + 1] & vm, b0, b1);
+          if constexpr (H16) {
+            float* o = st.o16[4 * cc + 2 * h];
+            mma_f16_16816(o, pv16[nb][0], pv16[nb][1], pv16[nb][2], pv16[nb][3], a0, a1);
+            mma_f16_16816(o + 4, pv16[nb][0], pv16[nb][1], pv16[nb][2], pv16[nb][3], b0, b1);
+          }
+          if constexpr (H8) mma_f16_16816(st.o8[2 * cc + h], a0, b0, a1, b1, pv8[nb][0], pv8[nb][1]);
+        }
+      }
+    }
+  }
+
+  // ---- low-rank values: Z += P U_i over each agent's own rows; U rows < a_i or >= seq_len selected out.
+  if (key0 + kQBlock <= a_first) return;
+  const bool one_pass = p.mode == LRKV_BASE_LR_SHARED && !boundary && a_max <= key0;
+  for (int ag = one_pass ? ag_hi : ag_lo; ag <= ag_hi; ++ag) {
+    const int a_i = one_pass ? 0 : a_sm[ag];
+    if (key0 + kQBlock <= a_i) continue;  // this U tile was not loaded
+    const uint32_t ub = Us + (p.mode == LRKV_BASE_SHARED ? ag : 0) * (kQBlock * RK * 2);
+    const bool clean = !boundary && a_i <= key0;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const int k16 = key0 + kw + 16 * nb;
+      if (k16 + 16 <= a_i || k16 >= sl) continue;  // warp-uniform
+      uint32_t um_lo = 0xFFFFFFFFu, um_hi = 0xFFFFFFFFu;
+      if (!clean) {
+        const int x = k_lo + 16 * nb, y = k_hi + 16 * nb;
+        um_lo = (x >= a_i && x < sl ? 0xFFFFu : 0u) | (x + 1 >= a_i && x + 1 < sl ? 0xFFFF0000u : 0u);
+        um_hi = (y >= a_i && y < sl ? 0xFFFFu : 0u) | (y + 1 >= a_i && y + 1 < sl ? 0xFFFF0000u : 0u);
+      }
+      uint32_t a16[4], b8[2];
+      if constexpr (H16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a16[i] = one_pass || my_ag[i & 1] == ag ? pz16[nb][i] : 0u;
+      }
+      if constexpr (H8) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) b8[i] = one_pass || my_ag[2 * H16] == ag ? pz8[nb][i] : 0u;
+      }
+      const int j = lane >> 3;
+      const int key = kw + 16 * nb + slot_key((j & 1) * 8 + (lane & 7));
+#pragma unroll
+      for (int mz = 0; mz < WR::MZ; ++mz) {
+        uint32_t r0, r1, r2 = 0, r3 = 0;  // ranks 16 mz + g8: slots 0-7, 8-15; ranks + 8 likewise
+        if constexpr (RK == 8) ldsm_x2_t(r0, r1, ub + u_at<RK>(key, 0));
+        else ldsm_x4_t(r0, r1, r2, r3, ub + u_at<RK>(key, 2 * mz + (j >> 1)));
+        r0 &= um_lo;
+        r1 &= um_hi;
+        r2 &= um_lo;
+        r3 &= um_hi;
+        if constexpr (H16) {
+          mma_bf16_16816(st.z16[RK == 8 ? 0 : 2 * mz], a16[0], a16[1], a16[2], a16[3], r0, r1);
+          if constexpr (RK > 8) mma_bf16_16816(st.z16[2 * mz + 1], a16[0], a16[1], a16[2], a16[3], r2, r3);
+        }
+        if constexpr (H8) mma_bf16_16816(st.z8[mz], r0, r2, r1, r3, b8[0], b8[1]);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the end of a segment
+// ---------------------------------------------------------------------------
+constexpr int kQThreads = kQWarps * 32;  // consumer threads
+__device__ __forceinline__ void q_sync() { named_bar_sync(1, kQThreads); }
+
+// Two records per CTA: 0 for the segment that starts the CTA's range, 1 for a later
+// one (only its last can be shared with the next CTA).
+__device__ __forceinline__ size_t q_record_slot(long long cta, long long cta_begin, long long item_t0) {
+  return 2 * cta + (item_t0 > cta_begin ? 1 : 0);
+}
+
+// Merge the warps' rows into the CTA's record rec = [m | l | O | Z] in shared
+// memory.  The warps of a row block held the same rows over different keys; sums
+// run in warp order, so the result does not depend on timing.
+template <int D, int RK, int H16, int H8, int NRB>
+__device__ __forceinline__ void merge_warps(WarpRows<D, RK, H16, H8>& st, float* rec, float* mb, float* ml, int rb,
+                                            int peer) {
+  using WR = WarpRows<D, RK, H16, H8>;
+  constexpr int RPW = WR::RPW, RP = RPW * NRB, NR = WR::NR, R8 = WR::R8;
+  constexpr int PEERS = kQWarps / NRB;
+  constexpr int CW = kQMergeCols;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
+  int row[NR];  // this lane's rows within the block
+#pragma unroll
+  for (int i = 0; i < NR; ++i) row[i] = i < R8 ? 8 * i + g8 : 16 * H16 + 2 * t4 + (i - R8);
+  float* my_ml = ml + warp * 2 * RPW;
+#pragma unroll
+  for (int i = 0; i < NR; ++i) {
+    const int lo = i < R8 ? 1 : 4, hi = i < R8 ? 2 : 16;
+#pragma unroll
+    for (int o = lo; o <= hi; o <<= 1) st.l[i] += __shfl_xor_sync(0xFFFFFFFFu, st.l[i], o);
+    if ((i < R8 ? t4 : g8) == 0) {
+      my_ml[row[i]] = st.m[i];
+      my_ml[RPW + row[i]] = st.l[i];
+    }
+  }
+  q_sync();
+  float fo[NR], fz[NR];
+#pragma unroll
+  for (int i = 0; i < NR; ++i) {
+    float M = kNegInf;
+#pragma unroll
+    for (int x = 0; x < PEERS; ++x) M = fmaxf(M, ml[(x * NRB + rb) * 2 * RPW + row[i]]);
+    fz[i] = st.m[i] == kNegInf ? 0.f : fast_exp2(st.m[i] - M);
+    // O stands for weights 2^(w - m) times larger; in two factors, since w - m can pass 127
+    const float h = st.m[i] == kNegInf || st.w[i] == kNegInf ? kNegInf : 0.5f * (st.w[i] - M);
+    fo[i] = fast_exp2(h);
+  }
+  if (tid < RP) {
+    const int b = tid / RPW, r = tid % RPW;
+    float M = kNegInf, L = 0.f;
+#pragma unroll
+    for (int x = 0; x < PEERS; ++x) M = fmaxf(M, ml[(x * NRB + b) * 2 * RPW + r]);
+#pragma unroll
+    for (int x = 0; x < PEERS; ++x) {
+      const float mm = ml[(x * NRB + b) * 2 * RPW + r];
+      L += mm == kNegInf ? 0.f : ml[(x * NRB + b) * 2 * RPW + RPW + r] * fast_exp2(mm - M);
+    }
+    rec[tid] = M;
+    rec[RP + tid] = L;
+  }
+  float* mine = mb + (peer * NRB + rb) * RPW * CW;
+  float* mO = rec + 2 * RP;
+  float* mZ = mO + RP * D;
+  auto reduce = [&](float* dst, int ld, int width) {  // dst[row][0 .. width) = sum over the peers
+    q_sync();
+    for (int e = 2 * tid; e < RP * width; e += 2 * kQThreads) {
+      const int r = e / width, col = e - r * width;
+      const float* src = mb + ((r / RPW) * RPW + r % RPW) * CW + col;
+      float2 a = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int x = 0; x < PEERS; ++x) {
+        const float2 v = *reinterpret_cast<const float2*>(src + x * NRB * RPW * CW);
+        a.x += v.x;
+        a.y += v.y;
+      }
+      *reinterpret_cast<float2*>(dst + r * ld + col) = a;
+    }
+    q_sync();
+  };
+#pragma unroll
+  for (int c0 = 0; c0 < D; c0 += CW) {
+    if constexpr (H16) {
+#pragma unroll
+      for (int x = 0; x < CW / 8; ++x)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float* o = st.o16[c0 / 8 + x];
+          *reinterpret_cast<float2*>(mine + row[i] * CW + 8 * x + 2 * t4) =
+              make_float2(o[2 * i] * fo[i] * fo[i], o[2 * i + 1] * fo[i] * fo[i]);
+        }
+    }
+    if constexpr (H8) {
+#pragma unroll
+      for (int x = 0; x < CW / 16; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = R8 + (e & 1);
+          mine[row[i] * CW + 16 * x + 8 * (e >> 1) + g8] = st.o8[c0 / 16 + x][e] * fo[i] * fo[i];
+        }
+    }
+    reduce(mO + c0, D, CW);
+  }
+  if constexpr (H16) {
+#pragma unroll
+    for (int x = 0; x < RK / 8; ++x)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        *reinterpret_cast<float2*>(mine + row[i] * CW + 8 * x + 2 * t4) =
+            make_float2(st.z16[x][2 * i] * fz[i], st.z16[x][2 * i + 1] * fz[i]);
+  }
+  if constexpr (H8) {
+#pragma unroll
+    for (int x = 0; x < WR::MZ; ++x)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (16 * x + 8 * (e >> 1) < RK)
+          mine[row[R8 + (e & 1)] * CW + 16 * x + 8 * (e >> 1) + g8] = st.z8[x][e] * fz[R8 + (e & 1)];
+  }
+  reduce(mZ, RK, RK);
+}
+
+// Publish the record, or, as the last of the item's CTAs to get here (ticket),
+// combine every record of the item; then out = (O + Z B_i,g) / l.
+template <int D, int RK, int RP>
+__device__ __forceinline__ void finish_item(const QDecodeParams& p, const Range& range, const Seg& sg, float* rec,
+                                            float* table, int* bcast) {
+  constexpr int REC = RP * (D + RK + 2);
+  constexpr int E4 = RP * (D + RK) / 4;
+  constexpr int PER = (E4 + kQThreads - 1) / kQThreads;
+  constexpr int TABLE = kQWarps * (RP > 16 && RP != 24 ? 16 : RP) * kQMergeCols;  // floats of the merge buffer
+  constexpr int CHUNK = TABLE / RP;                                               // records whose scales it holds
+  const int tid = threadIdx.x;
+  const bool shared = !range.whole && (sg.lo > 0 || sg.hi < sg.nt);
+  if (shared) {
+    const long long C = range.ctas, W = range.W;
+    const long long c_first = owner_cta(sg.item_t0, W, C), c_last = owner_cta(sg.item_t0 + sg.nt - 1, W, C);
+    const int segs = (int)(c_last - c_first + 1);
+    float* mine = p.partials + q_record_slot(blockIdx.x, range.t_begin, sg.item_t0) * REC;
+    for (int e = 4 * tid; e < REC; e += 4 * kQThreads)
+      __stcg(reinterpret_cast<float4*>(mine + e), *reinterpret_cast<const float4*>(rec + e));
+    q_sync();
+    if (tid == 0) {
+      __threadfence();
+      const int last = atomicAdd(p.tickets + sg.item, 1) == segs - 1;
+      if (last) p.tickets[sg.item] = 0;
+      *bcast = last;
+    }
+    q_sync();
+    if (!*bcast) return;
+    __threadfence();
+    auto record = [&](int j) {
+      const long long c = c_first + j;
+      return p.partials + q_record_slot(c, c * W / C, sg.item_t0) * REC;
+    };
+    if (tid < RP) {
+      float M = kNegInf;
+      for (int j = 0; j < segs; ++j) M = fmaxf(M, __ldcg(record(j) + tid));
+      rec[tid] = M;
+      rec[RP + tid] = 0.f;
+    }
+    float4 acc[PER];
+#pragma unroll
+    for (int u = 0; u < PER; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j0 = 0; j0 < segs; j0 += CHUNK) {
+      const int nj = min(CHUNK, segs - j0);
+      q_sync();
+      for (int e = tid; e < nj * RP; e += kQThreads) {
+        const float mj = __ldcg(record(j0 + e / RP) + e % RP);
+        table[e] = mj == kNegInf ? 0.f : fast_exp2(mj - rec[e % RP]);
+      }
+      q_sync();
+      if (tid < RP) {
+        float L = rec[RP + tid];
+        for (int j = 0; j < nj; ++j) L += __ldcg(record(j0 + j) + RP + tid) * table[j * RP + tid];
+        rec[RP + tid] = L;
+      }
+      for (int jb = 0; jb < nj; jb += kMergeBatch) {
+        float4 v[kMergeBatch][PER];
+#pragma unroll
+        for (int q = 0; q < kMergeBatch; ++q) {
+          if (jb + q >= nj) break;
+          const float4* src = reinterpret_cast<const float4*>(record(j0 + jb + q) + 2 * RP);
+#pragma unroll
+          for (int u = 0; u < PER; ++u)
+            if (tid + u * kQThreads < E4) v[q][u] = __ldcg(src + tid + u * kQThreads);
+        }
+#pragma unroll
+        for (int q = 0; q < kMergeBatch; ++q) {
+          if (jb + q >= nj) break;
+#pragma unroll
+          for (int u = 0; u < PER; ++u) {
+            const int e = 4 * (tid + u * kQThreads);
+            if (e >= 4 * E4) continue;
+            const float sc = table[(jb + q) * RP + (e < RP * D ? e / D : (e - RP * D) / RK)];
+            acc[u].x += v[q][u].x * sc;
+            acc[u].y += v[q][u].y * sc;
+            acc[u].z += v[q][u].z * sc;
+            acc[u].w += v[q][u].w * sc;
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+      const int e4 = tid + u * kQThreads;
+      if (e4 < E4) *reinterpret_cast<float4*>(rec + 2 * RP + 4 * e4) = acc[u];
+    }
+    q_sync();
+  }
+  // A thread takes (agent, two adjacent dims): the agent's B columns serve all its rows.
+  const float* mL = rec + RP;
+  const float* mO = rec + 2 * RP;
+  const float* mZ = mO + RP * D;
+  constexpr int D2 = D / 2;
+  const int HD = p.Hkv * D;
+  for (int u = tid; u < sg.n_ag * D2; u += kQThreads) {
+    const int agent = sg.i_lo + u / D2, dim = 2 * (u % D2);
+    const uint32_t* bp = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.b) +
+                                                           (size_t)agent * RK * HD + (size_t)sg.g * D + dim);
+    uint32_t b[RK];
+#pragma unroll
+    for (int r = 0; r < RK; ++r) b[r] = __ldg(bp + (size_t)r * (HD / 2));
+    const int r_end = min((agent + 1) * p.G - sg.row_lo, sg.rows);
+    for (int row = max(agent * p.G - sg.row_lo, 0); row < r_end; ++row) {
+      float2 o = *reinterpret_cast<const float2*>(mO + row * D + dim);
+#pragma unroll
+      for (int r = 0; r < RK; r += 4) {
+        const float4 z = *reinterpret_cast<const float4*>(mZ + row * RK + r);
+        o.x = fmaf(z.x, bf_lo(b[r]), o.x);
+        o.y = fmaf(z.x, bf_hi(b[r]), o.y);
+        o.x = fmaf(z.y, bf_lo(b[r + 1]), o.x);
+        o.y = fmaf(z.y, bf_hi(b[r + 1]), o.y);
+        o.x = fmaf(z.z, bf_lo(b[r + 2]), o.x);
+        o.y = fmaf(z.z, bf_hi(b[r + 2]), o.y);
+        o.x = fmaf(z.w, bf_lo(b[r + 3]), o.x);
+        o.y = fmaf(z.w, bf_hi(b[r + 3]), o.y);
+      }
+      const float L = mL[row], il = L == 0.f ? 0.f : 1.f / L;
+      o.x *= il;
+      o.y *= il;
+      const int grow = sg.row_lo + row;
+      const size_t at = (((size_t)sg.s * p.N + agent) * p.Hq + (size_t)sg.g * p.G + grow % p.G) * D + dim;
+      if (p.out_f32) *reinterpret_cast<float2*>(static_cast<float*>(p.out) + at) = o;
+      else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + at) = pack_bf16x2(o.x, o.y);
+    }
+  }
+}
+
+template <int FMT, int D, int RK, int H16, int H8, int NRB, int KPW>
+__device__ void q_consumers(const QDecodeParams& p, uint8_t* smem, const QDecodeSmem& lay, uint64_t* full,
+                            uint64_t* empty, volatile int* abort_flag, int* bcast, const Range& range) {
+  using WR = WarpRows<D, RK, H16, H8>;
+  constexpr int RPW = WR::RPW, RP = RPW * NRB, NR = WR::NR;
+  constexpr int KW = kQBlock / KPW;            // warps that share a tile's keys
+  constexpr int NG = kQWarps / (KW * NRB);     // groups that take tiles in turn
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2;
+  const int rb = warp % NRB, peer = warp / NRB;  // row block; place among the warps that hold its rows
+  const int og = peer / KW, kw = (peer % KW) * KPW;
+  float* rec = reinterpret_cast<float*>(smem + lay.rec_off);
+  float* mb = reinterpret_cast<float*>(smem + lay.mb_off);
+  float* ml = reinterpret_cast<float*>(smem + lay.ml_off);
+  const Meta* meta = reinterpret_cast<const Meta*>(smem + lay.meta_off);
+  int* a_sm = reinterpret_cast<int*>(smem + lay.a_off);
+  const uint32_t ring = smem_u32(smem);
+  int stage = 0, ntile = 0;
+  uint32_t phase = 0;
+  Walk walk;
+  walk.start(p, range);
+  Seg sg;
+  WR st;
+  while (walk.next(p, sg)) {
+    if (tid < sg.n_ag) a_sm[tid] = load_offset(p, sg.s, sg.i_lo + tid, true);
+    load_queries<D, RK, H16, H8>(p, sg, rb * RPW, st);
+    q_sync();
+    int a_max = 0, a_first = 0x7fffffff;
+    for (int j = 0; j < sg.n_ag; ++j) a_max = max(a_max, a_sm[j]);
+    // agents of this warp's rows, and of the rows whose weights this lane masks
+    const int w_lo = sg.row_lo + rb * RPW, w_rows = min(RPW, sg.rows - rb * RPW);
+    const int ag_lo = w_rows > 0 ? w_lo / p.G - sg.i_lo : 0;
+    const int ag_hi = w_rows > 0 ? (w_lo + w_rows - 1) / p.G - sg.i_lo : -1;
+    for (int ag = ag_lo; ag <= ag_hi; ++ag) a_first = min(a_first, a_sm[ag]);
+    int my_ag[2 * H16 + H8];
+#pragma unroll
+    for (int i = 0; i < 2 * H16 + H8; ++i) my_ag[i] = 8 * i + g8 < w_rows ? (w_lo + 8 * i + g8) / p.G - sg.i_lo : -1;
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      st.m[i] = st.w[i] = kNegInf;
+      st.l[i] = 0.f;
+    }
+    if constexpr (H16) {
+#pragma unroll
+      for (int x = 0; x < D / 8; ++x) st.o16[x][0] = st.o16[x][1] = st.o16[x][2] = st.o16[x][3] = 0.f;
+#pragma unroll
+      for (int x = 0; x < RK / 8; ++x) st.z16[x][0] = st.z16[x][1] = st.z16[x][2] = st.z16[x][3] = 0.f;
+    }
+    if constexpr (H8) {
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x) st.o8[x][0] = st.o8[x][1] = st.o8[x][2] = st.o8[x][3] = 0.f;
+#pragma unroll
+      for (int x = 0; x < WR::MZ; ++x) st.z8[x][0] = st.z8[x][1] = st.z8[x][2] = st.z8[x][3] = 0.f;
+    }
+
+    const int tiles_hi = sg.sl > 0 ? sg.hi : sg.lo;  // an empty session has no tiles
+    for (int tile = sg.lo; tile < tiles_hi; ++tile) {
+      const bool mine = NG == 1 || ntile % NG == og;
+      const int my_stage = stage;
+      const uint32_t my_phase = phase;
+      ++ntile;
+      if (++stage == p.stages) {
+        stage = 0;
+        phase ^= 1;
+      }
+      if (!mine) continue;
+      mbar_wait_bounded(&full[my_stage], my_phase, abort_flag, p.flags, p.spin_cap, true);
+      const Meta mt = meta[my_stage];
+      if (mt.ok)
+        q_tile<FMT, D, RK, H16, H8, KPW>(p, st, sg, ring + my_stage * lay.stage_bytes, mt, tile * kQBlock, kw, a_sm,
+                                         ag_lo, ag_hi, my_ag, a_first, a_max);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[my_stage]);
+    }
+    merge_warps<D, RK, H16, H8, NRB>(st, rec, mb, ml, rb, peer);
+    finish_item<D, RK, RP>(p, range, sg, rec, mb, bcast);
+    q_sync();  // the record, the merge buffer and the offsets are free again
+  }
+}
+
+// Three warpgroups: two of consumers, one whose first warp produces.  A thread is
+// launched with 168 registers (65536 / 384); the producers' share goes to the
+// consumers: 2 x 128 x 224 + 128 x 56 = 384 x 168.
+constexpr int kQBlockThreads = (kQWarps + 4) * 32;
+constexpr int kQConsumerRegs = 224, kQProducerRegs = 56;
+static_assert(kQThreads * kQConsumerRegs + 128 * kQProducerRegs <= kQBlockThreads * 168, "register split");
+
+template <int FMT, int D, int RK, int H16, int H8, int NRB, int KPW>
+__global__ void __launch_bounds__(kQBlockThreads, 1)
+    decode_quant_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                        const __grid_constant__ CUtensorMap tmU, const QDecodeParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const QDecodeSmem lay = q_smem_plan(D, RK, 16 * H16 + 8 * H8, NRB, p.n_u_slots, p.stages);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + lay.bar_off);
+  uint64_t* empty = full + p.stages;
+  Range* range = reinterpret_cast<Range*>(smem + lay.misc_off);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(range + 1);
+  int* bcast = const_cast<int*>(abort_flag) + 1;
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == kQWarps * 32) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&full[s], 2);                           // the tile's bytes; its scales
+      mbar_init(&empty[s], (kQBlock / KPW) * NRB);      // the warps that read the tile
+    }
+    *abort_flag = 0;
+    *bcast = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+    tma_prefetch_desc(&tmU);
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  if (warp == 0) find_range(p, range);
+  __syncthreads();
+  const Range r = *range;
+  if (warp >= kQWarps) {
+    setmaxnreg_dec<kQProducerRegs>();
+    if (warp == kQWarps)
+      q_producer<D, RK>(p, &tmK, &tmV, &tmU, smem, lay, reinterpret_cast<Meta*>(smem + lay.meta_off), full, empty,
+                        abort_flag, r);
+  } else {
+    setmaxnreg_inc<kQConsumerRegs>();
+    q_consumers<FMT, D, RK, H16, H8, NRB, KPW>(p, smem, lay, full, empty, abort_flag, bcast, r);
+  }
+}
+
+template <int FMT, int D, int RK, int H16, int H8, int NRB>
+lrkv_status launch_q(const QDecodeParams& p, const void* tmK, const void* tmV, const void* tmU, int smem, int ctas,
+                     cudaStream_t stream) {
+  constexpr int KPW = 16;
+  auto kern = decode_quant_kernel<FMT, D, RK, H16, H8, NRB, KPW>;
+  if (ensure_dynamic_smem<decode_quant_kernel<FMT, D, RK, H16, H8, NRB, KPW>>(smem) != cudaSuccess) return LRKV_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kQBlockThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const CUtensorMap& k = *static_cast<const CUtensorMap*>(tmK);
+  const CUtensorMap& v = *static_cast<const CUtensorMap*>(tmV);
+  const CUtensorMap& u = *static_cast<const CUtensorMap*>(tmU);
+  return cudaLaunchKernelEx(&cfg, kern, k, v, u, p) == cudaSuccess ? LRKV_OK : LRKV_ERR_CUDA;
+}
+
+template <int FMT, int D, int RK>
+lrkv_status dispatch_rows(const QDecodeParams& p, int rows, const void* tmK, const void* tmV, const void* tmU,
+                          int smem, int ctas, cudaStream_t st) {
+  if (rows <= 8) return launch_q<FMT, D, RK, 0, 1, 1>(p, tmK, tmV, tmU, smem, ctas, st);
+  if (rows <= 16) return launch_q<FMT, D, RK, 1, 0, 1>(p, tmK, tmV, tmU, smem, ctas, st);
+  if (rows <= 24) return launch_q<FMT, D, RK, 1, 1, 1>(p, tmK, tmV, tmU, smem, ctas, st);
+  return launch_q<FMT, D, RK, 1, 0, 2>(p, tmK, tmV, tmU, smem, ctas, st);
+}
+
+}  // namespace
+
+template <int FMT, int D>
+lrkv_status launch_decode_quant_fd(const QDecodeParams& p, int RK, int rows, const void* tmK, const void* tmV,
+                                   const void* tmU, int smem, int ctas, void* stream) {
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (RK == 8) return dispatch_rows<FMT, D, 8>(p, rows, tmK, tmV, tmU, smem, ctas, st);
+  if (RK == 16) return dispatch_rows<FMT, D, 16>(p, rows, tmK, tmV, tmU, smem, ctas, st);
+  return dispatch_rows<FMT, D, 32>(p, rows, tmK, tmV, tmU, smem, ctas, st);
+}
+
+}  // namespace lrkv

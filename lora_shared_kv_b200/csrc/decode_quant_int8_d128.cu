@@ -1,0 +1,7 @@
+// Decode over an 8-bit cache: int8 codes, head_dim 128.
+#include "decode_quant.cuh"
+
+namespace lrkv {
+template lrkv_status launch_decode_quant_fd<LRKV_Q_INT8, 128>(const QDecodeParams&, int, int, const void*, const void*,
+                                                      const void*, int, int, void*);
+}

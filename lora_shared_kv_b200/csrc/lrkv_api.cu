@@ -12,10 +12,12 @@
 
 #include <vector>
 
+#include "api_common.h"
 #include "lrkv_internal.h"
 #include "prefill.h"
 
-namespace {
+namespace lrkv {
+namespace api {
 
 thread_local char g_detail[512] = "";
 
@@ -42,17 +44,9 @@ lrkv_status cuda_fail(cudaError_t e, const char* what) {
   return fail(LRKV_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 // ---------------------------------------------------------------------------
 // device facts
 // ---------------------------------------------------------------------------
-struct DeviceInfo {
-  int sms = 0;
-  int major = 0;
-  int smem_optin = 0;
-};
-
 lrkv_status device_info(DeviceInfo* out) {
   static std::mutex mu;
   static DeviceInfo cache[64];
@@ -98,18 +92,17 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// 4-D bf16 tensor map, dims/strides innermost first (strides in elements,
-// for dims 1..3).  A dimension of extent 1 gets a packed stride.
 lrkv_status make_map4(CUtensorMap* m, const void* base, const uint64_t dims[4], const int64_t strides_el[3],
-                      const uint32_t box[4], CUtensorMapSwizzle swz, const char* what) {
+                      const uint32_t box[4], CUtensorMapSwizzle swz, const char* what, CUtensorMapDataType type,
+                      int elem_bytes) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return fail(LRKV_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   cuuint64_t gdim[4];
   cuuint64_t gstr[3];
-  uint64_t packed = dims[0] * 2;
+  uint64_t packed = dims[0] * elem_bytes;
   for (int i = 0; i < 4; ++i) gdim[i] = dims[i];
   for (int i = 0; i < 3; ++i) {
-    uint64_t s = strides_el[i] > 0 ? (uint64_t)strides_el[i] * 2 : 0;
+    uint64_t s = strides_el[i] > 0 ? (uint64_t)strides_el[i] * elem_bytes : 0;
     if (dims[i + 1] == 1 || s == 0) s = packed < 16 ? 16 : (packed + 15) / 16 * 16;
     if (s % 16 != 0) return fail(LRKV_ERR_MISALIGNED, "%s: stride %d (%llu bytes) is not a multiple of 16 bytes", what, i + 1, (unsigned long long)s);
     gstr[i] = s;
@@ -117,7 +110,7 @@ lrkv_status make_map4(CUtensorMap* m, const void* base, const uint64_t dims[4], 
   }
   cuuint32_t bx[4] = {box[0], box[1], box[2], box[3]};
   cuuint32_t es[4] = {1, 1, 1, 1};
-  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), gdim, gstr, bx, es,
+  CUresult r = fn(m, type, 4, const_cast<void*>(base), gdim, gstr, bx, es,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(LRKV_ERR_INVALID_ARGUMENT, "%s: cuTensorMapEncodeTiled failed (%d)", what, (int)r);
@@ -170,6 +163,13 @@ lrkv_status check_u(const lrkv_u_view* u, const lrkv_problem* p, int rows_needed
   if (u->num_rows < rows_needed) return fail(LRKV_ERR_INVALID_ARGUMENT, "u num_rows %d < %d rows needed", u->num_rows, rows_needed);
   return LRKV_OK;
 }
+
+}  // namespace api
+}  // namespace lrkv
+
+using namespace lrkv::api;
+
+namespace {
 
 // ---------------------------------------------------------------------------
 // decode plan
@@ -369,9 +369,9 @@ lrkv_status read_device_flags(const void* workspace, int32_t clear, uint32_t* fl
   }
   if (flags_out) *flags_out = flags;
   if (flags & LRKV_DEVFLAG_TIMEOUT) return fail(LRKV_ERR_TIMEOUT, "a bounded wait inside a kernel gave up (flags 0x%x)", flags);
-  if (flags) return fail(LRKV_ERR_DEVICE_FAULT, "device-side checks flagged bad data (flags 0x%x: %s%s%s)", flags,
+  if (flags) return fail(LRKV_ERR_DEVICE_FAULT, "device-side checks flagged bad data (flags 0x%x: %s%s%s%s)", flags,
                          (flags & LRKV_DEVFLAG_SEQLEN) ? "seq_len " : "", (flags & LRKV_DEVFLAG_OFFSET) ? "offset " : "",
-                         (flags & LRKV_DEVFLAG_PAGE) ? "page-id" : "");
+                         (flags & LRKV_DEVFLAG_PAGE) ? "page-id " : "", (flags & LRKV_DEVFLAG_NONFINITE) ? "non-finite" : "");
   return LRKV_OK;
 }
 

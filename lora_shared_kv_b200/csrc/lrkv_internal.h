@@ -11,6 +11,7 @@
 #define LRKV_DEVFLAG_OFFSET 0x2u    // a negative aLoRA offset (treated as 0)
 #define LRKV_DEVFLAG_PAGE 0x4u      // a page id outside [0, num_pages) (tile skipped)
 #define LRKV_DEVFLAG_TIMEOUT 0x8u   // a bounded wait gave up
+#define LRKV_DEVFLAG_NONFINITE 0x10u  // an infinity or NaN was quantised
 
 namespace lrkv {
 

@@ -1,0 +1,130 @@
+// Internal definitions of the operators on an 8-bit K/V cache.
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "lrkv_internal.h"
+
+namespace lrkv {
+
+constexpr int kQBlock = LRKV_QUANT_BLOCK;  // tokens that share a scale, keys of a decode tile, tokens of a page
+static_assert(kQBlock == kKeysPerTile, "a decode tile is one block of the cache");
+
+// ---------------------------------------------------------------------------
+// writing and reading back
+// ---------------------------------------------------------------------------
+struct QCacheParams {
+  // the bf16 side (source of a write, destination of a read)
+  uint16_t* x[2];            // K, V
+  long long x_ss, x_sh, x_st, x_sp;
+  const int32_t* x_table;    // null => dense
+  long long x_pt;
+  int x_pages;
+  // the 8-bit side
+  uint8_t* c[2];
+  float* scale[2];
+  long long c_ss, c_sh, c_st, c_sp;
+  long long s_ss, s_sh, s_sp;
+  const int32_t* c_table;
+  long long c_pt;
+  int c_pages;
+  int rows;                  // row capacity of a session
+  const int32_t* first;      // [S] or null
+  const int32_t* count;      // [S] or null
+  int S, Hkv, T;
+  int nblk;                  // blocks that a session's rows can touch
+  unsigned* flags;
+};
+
+lrkv_status launch_quantize(const QCacheParams& p, int D, int fmt, void* stream);
+lrkv_status launch_dequantize(const QCacheParams& p, int D, int fmt, void* stream);
+
+// ---------------------------------------------------------------------------
+// decode
+// ---------------------------------------------------------------------------
+struct QDecodeParams {
+  const void* q;             // bf16 [S, N, Hq, d]
+  const void* b;             // bf16 [N, r, Hkv*d]
+  const int32_t* seq_lens;   // [S]
+  const int32_t* offsets;    // [S, N] or null
+  const float* k_scale;
+  const float* v_scale;
+  long long s_ss, s_sh, s_sp;
+  const int32_t* page_table; // null => dense
+  long long pt_stride;
+  void* out;
+  int out_f32;
+  int S, N, Hq, Hkv, G;
+  int rows_total;            // N * G
+  int rows_per_group;        // rows of one work item (<= kMaxRowsPerItem)
+  int n_rg;                  // row groups per (session, KV head)
+  int n_u_slots;             // U tiles staged per K/V tile
+  int mode;
+  int max_seq_len;
+  int u_rows;
+  int num_pages;
+  int stages;
+  int whole_slack;           // see q_whole_items
+  float scale_log2;          // softmax_scale * log2(e)
+  float* partials;           // two records per CTA: see q_record_slot
+  int* tickets;              // one per work item
+  unsigned* flags;
+  unsigned spin_cap;         // failure-detection test hook, as in DecodeParams
+  int stall;
+};
+
+// Consumer warps of the decode kernel.  A warp holds the query rows of one row
+// block in one of three shapes: up to 8 rows (keys as the MMA's M), up to 16
+// (rows as M), up to 24 (16 + 8).  Items of 25 to 32 rows take two row blocks of
+// 16.  The warps of a row block split a tile's 64 keys.
+constexpr int kQWarps = 8;
+
+struct QShape {
+  int h16, h8, nrb;          // 16-row part, 8-row part, row blocks
+};
+
+__host__ __device__ constexpr QShape q_shape(int rows) {
+  return rows <= 8 ? QShape{0, 1, 1} : rows <= 16 ? QShape{1, 0, 1} : rows <= 24 ? QShape{1, 1, 1} : QShape{1, 0, 2};
+}
+
+// Columns of O that the warps exchange per pass when their rows are merged.
+constexpr int kQMergeCols = 32;
+
+// Shared-memory plan (bytes from a 1024-aligned base).
+struct QDecodeSmem {
+  int stage_bytes, rec_off, mb_off, ml_off, meta_off, a_off, bar_off, misc_off, total;
+};
+
+__host__ __device__ inline QDecodeSmem q_smem_plan(int D, int RK, int rows_block, int nrb, int n_u_slots, int stages) {
+  QDecodeSmem s;
+  const int RP = rows_block * nrb;
+  s.stage_bytes = round_up(2 * kQBlock * D + n_u_slots * kQBlock * RK * 2, 1024);
+  s.rec_off = stages * s.stage_bytes;                                    // [m | l | O | Z] of RP rows
+  s.mb_off = s.rec_off + RP * (D + RK + 2) * 4;                          // the warps' columns being merged
+  s.ml_off = s.mb_off + kQWarps * rows_block * kQMergeCols * 4;          // the warps' m and l
+  s.meta_off = round_up(s.ml_off + kQWarps * rows_block * 2 * 4, 16);    // {k scale, v scale, ok} of each stage
+  s.a_off = s.meta_off + stages * 16;                                    // offsets of the item's agents
+  s.bar_off = round_up(s.a_off + kMaxAgents * 4, 16);
+  s.misc_off = s.bar_off + 2 * stages * 8;                               // the CTA's range, abort word, broadcast word
+  s.total = s.misc_off + 96;
+  return s;
+}
+
+inline size_t q_record_floats(int RP, int D, int RK) { return (size_t)RP * (D + RK + 2); }
+
+// A CTA takes whole items, one each, when there are no more items than CTAs and
+// the longest item is at most `slack` tiles above the even share: nothing is
+// then published or merged.
+__host__ __device__ inline bool q_whole_items(long long items, long long ctas, long long nt_max, long long W, int slack) {
+  return items <= ctas && nt_max <= (W + ctas - 1) / ctas + slack;
+}
+
+lrkv_status launch_decode_quant(const QDecodeParams& p, int D, int RK, int rows, int fmt, const void* tmK,
+                                const void* tmV, const void* tmU, int smem_bytes, int ctas, void* stream);
+// One translation unit per (format, head_dim), so that they compile in parallel.
+template <int FMT, int D>
+lrkv_status launch_decode_quant_fd(const QDecodeParams& p, int RK, int rows, const void* tmK, const void* tmV,
+                                   const void* tmU, int smem_bytes, int ctas, void* stream);
+
+}  // namespace lrkv
