@@ -60,10 +60,12 @@ struct Range {
   int pad;
 };
 
-// Stage facts that do not come through the tile copies.
+// Stage facts that do not come through the tile copies.  `n` is the number of the
+// tile in the stage: a consumer waits for its own there before it waits on the
+// stage's mbarrier, so that a parity wait is never satisfied by an older phase.
 struct Meta {
   float ks, vs;
-  int ok, pad;
+  int ok, n;
 };
 
 __device__ __forceinline__ int clamp_len(const QDecodeParams& p, int sl) {
@@ -196,6 +198,51 @@ struct Walk {
   }
 };
 
+// Visiting order of an item's tiles.  Tiles past the agents' offsets carry the
+// low-rank work, so runs of kTileRun tiles (contiguous in HBM) are visited in the
+// order (j stride) mod runs with a stride near 0.618 of the run count and coprime to
+// it: every contiguous stretch of the order then covers the item evenly, and so
+// does every CTA's share.  A partial last run stays in place.
+struct QOrder {
+  int runs, stride, j, r, w;
+  __device__ __forceinline__ void start(int nt, int k0, bool balance) {
+    runs = nt / kTileRun;
+    stride = 1;
+    if (balance && runs > 2) {
+      stride = (int)(0.618f * runs) | 1;
+      for (;;) {
+        int x = stride, y = runs;
+        while (y) {
+          const int z = x % y;
+          x = y;
+          y = z;
+        }
+        if (x == 1) break;
+        stride += 2;
+      }
+      if (stride >= runs) stride = 1;
+    }
+    j = k0 / kTileRun;
+    w = k0 - j * kTileRun;
+    r = j < runs ? (int)((long long)j * stride % runs) : j;
+  }
+  __device__ __forceinline__ int tile() const { return r * kTileRun + w; }
+  // the tile k places on
+  __device__ __forceinline__ int ahead(int k) const {
+    const int at = j * kTileRun + w + k, ja = at / kTileRun;
+    return (ja < runs ? (int)((long long)ja * stride % runs) : ja) * kTileRun + at % kTileRun;
+  }
+  __device__ __forceinline__ void next() {
+    if (++w == kTileRun) {
+      w = 0;
+      ++j;
+      r += stride;
+      if (r >= runs) r -= runs;
+      if (j >= runs) r = j;
+    }
+  }
+};
+
 __device__ __forceinline__ int load_offset(const QDecodeParams& p, int s, int agent, bool flag_errors) {
   if (p.offsets == nullptr) return 0;
   int a = __ldg(p.offsets + (size_t)s * p.N + agent);
@@ -210,19 +257,28 @@ __device__ __forceinline__ int load_offset(const QDecodeParams& p, int s, int ag
 // producer warp
 // ---------------------------------------------------------------------------
 // Tile n of the CTA goes to ring stage n % stages.  A stage is full after two
-// arrivals: the bytes of the tile copies, and the two scales' 4-byte copies.
+// arrivals: the bytes of the K/V copies, and the two scales' 4-byte copies.  Tiles
+// that reach past an offset take a stage of the U ring too; tiles without one then
+// do not hold its space.
+struct QBars {
+  uint64_t *full, *empty, *u_full, *u_empty;
+  Meta* meta;
+  volatile int* useq;
+  volatile int* abort_flag;
+};
+
 template <int D, int RK>
 __device__ void q_producer(const QDecodeParams& p, const CUtensorMap* tmK, const CUtensorMap* tmV,
-                           const CUtensorMap* tmU, uint8_t* ring, const QDecodeSmem& lay, Meta* meta, uint64_t* full,
-                           uint64_t* empty, volatile int* abort_flag, const Range& range) {
+                           const CUtensorMap* tmU, uint8_t* smem, const QDecodeSmem& lay, const QBars& bar,
+                           const Range& range) {
   const int lane = threadIdx.x & 31;
   const uint64_t pol_kv = policy_evict_first();
   const uint64_t pol_u = policy_evict_last();
   constexpr int KV_BYTES = kQBlock * D;
   constexpr int U_BYTES = kQBlock * RK * 2;
   const bool paged = p.page_table != nullptr;
-  int stage = 0, n = 0;
-  uint32_t phase = 0;
+  int stage = 0, n = 0, us = 0, un = 0;
+  uint32_t phase = 0, uphase = 0;
   bool stop = p.stall != 0;  // the test hook: issue nothing, so the consumers' waits run out
   Walk walk;
   walk.start(p, range);
@@ -231,45 +287,42 @@ __device__ void q_producer(const QDecodeParams& p, const CUtensorMap* tmK, const
     if (sg.sl == 0) continue;
     const int my_a = lane < sg.n_ag ? load_offset(p, sg.s, sg.i_lo + lane, false) : 0x7fffffff;
     int ids = 0;
-    for (int tile = sg.lo; tile < sg.hi; ++tile) {
-      const int k = tile - sg.lo;
+    QOrder ord;
+    ord.start(sg.nt, sg.lo, p.balance && !range.whole);
+    for (int k = 0; k < sg.hi - sg.lo; ++k, ord.next()) {
+      const int tile = ord.tile();
       if (paged && (k & 31) == 0)  // page ids of the next 32 tiles, one per lane
-        ids = tile + lane < sg.hi ? __ldg(p.page_table + (size_t)sg.s * p.pt_stride + tile + lane) : 0;
+        ids = k + lane < sg.hi - sg.lo ? __ldg(p.page_table + (size_t)sg.s * p.pt_stride + ord.ahead(lane)) : 0;
       const int page = paged ? __shfl_sync(0xFFFFFFFFu, ids, k & 31) : 0;
       const unsigned need = __ballot_sync(0xFFFFFFFFu, lane < sg.n_ag && (tile + 1) * kQBlock > my_a);
       const bool ok = !paged || (page >= 0 && page < p.num_pages);
-      const unsigned umask = !ok ? 0u : p.mode == LRKV_BASE_SHARED ? need : (need ? 1u : 0u);
-      const bool freed = mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, p.flags, p.spin_cap, true);
+      bool freed = mbar_wait_bounded(&bar.empty[stage], phase ^ 1, bar.abort_flag, p.flags, p.spin_cap, true);
       // After an abort the consumers release stages without waiting for their
       // copies, so nothing more may be issued; the whole warp leaves together.
-      if (__any_sync(0xFFFFFFFFu, !freed || *abort_flag)) {
+      if (__any_sync(0xFFFFFFFFu, !freed || *bar.abort_flag)) {
         stop = true;
         break;
       }
+      const long long sc = paged ? page * p.s_sp + sg.g * p.s_sh : sg.s * p.s_ss + sg.g * p.s_sh + tile;
+      const int c3 = paged ? page : sg.s;
       if (lane == 0) {
-        uint8_t* st = ring + (size_t)stage * lay.stage_bytes;
-        meta[stage].ok = ok;
+        uint64_t* full = &bar.full[stage];
+        Meta* meta = &bar.meta[stage];
+        meta->ok = ok;
+        *reinterpret_cast<volatile int*>(&meta->n) = n;
         if (!ok) {
           atomicOr(p.flags, LRKV_DEVFLAG_PAGE);
-          mbar_arrive(&full[stage]);
-          mbar_arrive(&full[stage]);
+          mbar_arrive(full);
+          mbar_arrive(full);
         } else {
-          const long long sc = paged ? page * p.s_sp + sg.g * p.s_sh : sg.s * p.s_ss + sg.g * p.s_sh + tile;
-          mbar_arrive_expect_tx(&full[stage], 2 * KV_BYTES + __popc(umask) * U_BYTES);
+          uint8_t* st = smem + (size_t)stage * lay.tile_bytes;
           const int c1 = paged ? 0 : tile * kQBlock;
-          const int c3 = paged ? page : sg.s;
-          tma_load_4d(st, tmK, &full[stage], 0, c1, sg.g, c3, pol_kv);
-          tma_load_4d(st + KV_BYTES, tmV, &full[stage], 0, c1, sg.g, c3, pol_kv);
-          cp_async4(smem_u32(&meta[stage].ks), p.k_scale + sc);
-          cp_async4(smem_u32(&meta[stage].vs), p.v_scale + sc);
-          cp_async_mbar_arrive(&full[stage]);
-          unsigned m = umask;
-          while (m) {
-            const int slot = __ffs(m) - 1;
-            m &= m - 1;
-            tma_load_4d(st + 2 * KV_BYTES + slot * U_BYTES, tmU, &full[stage], 0, tile * kQBlock,
-                        p.mode == LRKV_BASE_SHARED ? sg.i_lo + slot : 0, sg.s, pol_u);
-          }
+          mbar_arrive_expect_tx(full, 2 * KV_BYTES);
+          tma_load_4d(st, tmK, full, 0, c1, sg.g, c3, pol_kv);
+          tma_load_4d(st + KV_BYTES, tmV, full, 0, c1, sg.g, c3, pol_kv);
+          cp_async4(smem_u32(&meta->ks), p.k_scale + sc);
+          cp_async4(smem_u32(&meta->vs), p.v_scale + sc);
+          cp_async_mbar_arrive(full);
         }
       }
       __syncwarp();
@@ -278,25 +331,52 @@ __device__ void q_producer(const QDecodeParams& p, const CUtensorMap* tmK, const
         stage = 0;
         phase ^= 1;
       }
+      if (need) {
+        freed = mbar_wait_bounded(&bar.u_empty[us], uphase ^ 1, bar.abort_flag, p.flags, p.spin_cap, true);
+        if (__any_sync(0xFFFFFFFFu, !freed || *bar.abort_flag)) {
+          stop = true;
+          break;
+        }
+        if (lane == 0) {
+          uint64_t* full = &bar.u_full[us];
+          unsigned m = !ok ? 0u : p.mode == LRKV_BASE_SHARED ? need : 1u;
+          bar.useq[us] = un;
+          if (m) mbar_arrive_expect_tx(full, __popc(m) * U_BYTES);
+          else mbar_arrive(full);
+          while (m) {
+            const int slot = __ffs(m) - 1;
+            m &= m - 1;
+            tma_load_4d(smem + lay.u_off + us * lay.u_bytes + slot * U_BYTES, tmU, full, 0, tile * kQBlock,
+                        p.mode == LRKV_BASE_SHARED ? sg.i_lo + slot : 0, sg.s, pol_u);
+          }
+        }
+        __syncwarp();
+        ++un;
+        if (++us == p.u_stages) {
+          us = 0;
+          uphase ^= 1;
+        }
+      }
     }
   }
   // After an abort the consumers may stop waiting; no copy of this CTA may still
   // be landing in shared memory when it exits.
   if (lane == 0) {
     cp_async_wait<0>();
-    if (*abort_flag) {
-      const int m = n < p.stages ? n : p.stages;
-      int st = stage;
-      uint32_t ph = phase;
-      for (int j = 0; j < m; ++j) {
-        if (--st < 0) {
-          st = p.stages - 1;
-          ph ^= 1;
+    if (*bar.abort_flag) {
+      auto drain = [](uint64_t* full, int stages, int issued, int st, uint32_t ph) {
+        for (int j = 0; j < (issued < stages ? issued : stages); ++j) {
+          if (--st < 0) {
+            st = stages - 1;
+            ph ^= 1;
+          }
+          uint32_t spins = 0;
+          while (!mbar_try_wait(&full[st], ph) && ++spins < kSpinCap) {
+          }
         }
-        uint32_t spins = 0;
-        while (!mbar_try_wait(&full[st], ph) && ++spins < kSpinCap) {
-        }
-      }
+      };
+      drain(bar.full, p.stages, n, stage, phase);
+      drain(bar.u_full, p.u_stages, un, us, uphase);
     }
   }
 }
@@ -313,8 +393,11 @@ struct WarpRows {
   // rows 2 t4 and 2 t4 + 1.  Index 0, 1: the first; 2, 3: the second part's.
   static constexpr int NR = 2 * (H16 + H8);
   static constexpr int R8 = 2 * H16;             // first index of the 8-row part
-  uint32_t q16[H16 ? KS : 1][4];
-  uint32_t q8[H8 ? KS : 1][2];
+  // A 24-row block keeps its query fragments in shared memory: its accumulators
+  // leave no registers for them.
+  static constexpr bool QS = H16 && H8;
+  uint32_t q16[H16 && !QS ? KS : 1][4];
+  uint32_t q8[H8 && !QS ? KS : 1][2];
   float c[NR];      // what turns a row's raw score into log2 units, without the block's key scale
   float m[NR];      // softmax reference (log2 units) of l and Z
   float w[NR];      // reference of O
@@ -347,7 +430,8 @@ __device__ __forceinline__ const __nv_bfloat16* q_row(const QDecodeParams& p, co
 // are 4 t4 .. + 3 (the bytes that ldmatrix gives it of K).
 template <int D, int RK, int H16, int H8>
 __device__ __forceinline__ void load_queries(const QDecodeParams& p, const Seg& sg, int rbase,
-                                             WarpRows<D, RK, H16, H8>& st) {
+                                             WarpRows<D, RK, H16, H8>& st, uint32_t* qs) {
+  using WR = WarpRows<D, RK, H16, H8>;
   constexpr int KS = D / 16;
   const int lane = threadIdx.x & 31, g8 = lane >> 2, t4 = lane & 3;
   constexpr int PARTS = 2 * H16 + H8;  // rows whose elements this lane holds
@@ -373,16 +457,32 @@ __device__ __forceinline__ void load_queries(const QDecodeParams& p, const Seg& 
   }
 #pragma unroll
   for (int ks = 0; ks < KS; ++ks) {
+    uint32_t f16[4] = {}, f8[2] = {};
 #pragma unroll
     for (int i = 0; i < PARTS; ++i) {
       const uint32_t lo = pack_f16x2(bf_lo(raw[i][ks].x) * f[i], bf_hi(raw[i][ks].x) * f[i]);
       const uint32_t hi = pack_f16x2(bf_lo(raw[i][ks].y) * f[i], bf_hi(raw[i][ks].y) * f[i]);
       if (H16 && i < 2) {
-        st.q16[ks][i] = lo;
-        st.q16[ks][i + 2] = hi;
+        f16[i] = lo;
+        f16[i + 2] = hi;
       } else {
-        st.q8[ks][0] = lo;
-        st.q8[ks][1] = hi;
+        f8[0] = lo;
+        f8[1] = hi;
+      }
+    }
+    if constexpr (WR::QS) {  // every warp of the block holds the same: one writes
+      if (threadIdx.x < 32) {
+        *reinterpret_cast<uint4*>(qs + (ks * 32 + lane) * 4) = make_uint4(f16[0], f16[1], f16[2], f16[3]);
+        *reinterpret_cast<uint2*>(qs + KS * 128 + (ks * 32 + lane) * 2) = make_uint2(f8[0], f8[1]);
+      }
+    } else {
+      if constexpr (H16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) st.q16[ks][i] = f16[i];
+      }
+      if constexpr (H8) {
+        st.q8[ks][0] = f8[0];
+        st.q8[ks][1] = f8[1];
       }
     }
   }
@@ -411,20 +511,20 @@ __device__ __forceinline__ uint32_t u_at(int k, int c) {
 
 __device__ __forceinline__ int slot_key(int s) { return s ^ ((s & 8) >> 1); }
 
-// One warp's KPW keys (from key kw of the tile on) of one tile.
-template <int FMT, int D, int RK, int H16, int H8, int KPW>
-__device__ __forceinline__ void q_tile(const QDecodeParams& p, WarpRows<D, RK, H16, H8>& st, const Seg& sg,
-                                       uint32_t Ks, const Meta& mt, int key0, int kw, const int* a_sm, int ag_lo,
-                                       int ag_hi, const int* my_ag, int a_first, int a_max) {
+// Scores, softmax and values of one warp's keys (kw .. of the tile) of one tile; the
+// weights for the low-rank product are left in pz16 (rows as M) and pz8.  LAST: the
+// tile reaches past seq_len.
+template <int FMT, int D, int RK, int H16, int H8, bool LAST>
+__device__ __forceinline__ void q_tile(WarpRows<D, RK, H16, H8>& st, int sl, uint32_t Ks, float ks_scale,
+                                       float vs_scale, int key0, int kw, const uint32_t* qs,
+                                       uint32_t (*pz16)[4], uint32_t (*pz8)[2]) {
   using WR = WarpRows<D, RK, H16, H8>;
   constexpr int KS = D / 16;
-  constexpr int NB = KPW / 16;  // blocks of 16 keys
+  constexpr int NB = kQWarpKeys / 16;  // blocks of 16 keys
   constexpr int NR = WR::NR;
   constexpr int R8 = WR::R8;
   const int lane = threadIdx.x & 31, g8 = lane >> 2, t4 = lane & 3;
   const uint32_t Vs = Ks + kQBlock * D;
-  const uint32_t Us = Vs + kQBlock * D;
-  const int sl = sg.sl;
 
   // ---- scores: S = Q K^T (16-row part), S^T = K Q^T (8-row part)
   float s16[H16 ? NB : 1][2][4], s8[H8 ? NB : 1][4];
@@ -436,34 +536,59 @@ __device__ __forceinline__ void q_tile(const QDecodeParams& p, WarpRows<D, RK, H
       if constexpr (H8) s8[nb][e] = 0.f;
     }
   {
-    const int j = lane >> 3, key = kw + slot_key((j & 1) * 8 + (lane & 7));
+    // tiles are 1024-aligned and a row's chunk bits lie below its key bits, so
+    // chunk 2 cc + c of a row is chunk c's address with bits 5 .. flipped by cc
+    const int j = lane >> 3;
+    const uint32_t at = Ks + tile_at<D>(kw + slot_key((j & 1) * 8 + (lane & 7)), j >> 1);
 #pragma unroll
     for (int cc = 0; cc < KS / 2; ++cc) {
+      uint32_t q16[H16 ? 2 : 1][4], q8[H8 ? 2 : 1][2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int ks = 2 * cc + h;
+        if constexpr (WR::QS) {
+          const uint4 a = *reinterpret_cast<const uint4*>(qs + (ks * 32 + lane) * 4);
+          const uint2 b = *reinterpret_cast<const uint2*>(qs + KS * 128 + (ks * 32 + lane) * 2);
+          q16[h][0] = a.x;
+          q16[h][1] = a.y;
+          q16[h][2] = a.z;
+          q16[h][3] = a.w;
+          q8[h][0] = b.x;
+          q8[h][1] = b.y;
+        } else {
+          if constexpr (H16) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) q16[h][i] = st.q16[ks][i];
+          }
+          if constexpr (H8) {
+            q8[h][0] = st.q8[ks][0];
+            q8[h][1] = st.q8[ks][1];
+          }
+        }
+      }
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         uint32_t r[4];  // chunk 2cc: slots 0-7, 8-15; chunk 2cc + 1 likewise
-        ldsm_x4(r[0], r[1], r[2], r[3], Ks + tile_at<D>(key + 16 * nb, 2 * cc + (j >> 1)));
+        ldsm_x4(r[0], r[1], r[2], r[3], (at ^ (cc << 5)) + nb * 16 * D);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t a0, a2, b0, b2;
           codes_to_half2<FMT>(r[2 * h], a0, a2);
           codes_to_half2<FMT>(r[2 * h + 1], b0, b2);
-          const int ks = 2 * cc + h;
           if constexpr (H16) {
-            mma_f16_16816(s16[nb][0], st.q16[ks][0], st.q16[ks][1], st.q16[ks][2], st.q16[ks][3], a0, a2);
-            mma_f16_16816(s16[nb][1], st.q16[ks][0], st.q16[ks][1], st.q16[ks][2], st.q16[ks][3], b0, b2);
+            mma_f16_16816(s16[nb][0], q16[h][0], q16[h][1], q16[h][2], q16[h][3], a0, a2);
+            mma_f16_16816(s16[nb][1], q16[h][0], q16[h][1], q16[h][2], q16[h][3], b0, b2);
           }
-          if constexpr (H8) mma_f16_16816(s8[nb], a0, b0, a2, b2, st.q8[ks][0], st.q8[ks][1]);
+          if constexpr (H8) mma_f16_16816(s8[nb], a0, b0, a2, b2, q8[h][0], q8[h][1]);
         }
       }
     }
   }
 
   // ---- softmax
-  const bool boundary = key0 + kQBlock > sl;
   const int k_lo = key0 + kw + 2 * t4;                 // keys of slots 2 t4 (+ 1)
   const int k_hi = key0 + kw + 8 + ((2 * t4) ^ 4);     // keys of slots 2 t4 + 8 (+ 9)
-  if (boundary) {  // keys at or past seq_len are selected out
+  if constexpr (LAST) {  // keys at or past seq_len are selected out
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       if constexpr (H16) {
@@ -483,7 +608,7 @@ __device__ __forceinline__ void q_tile(const QDecodeParams& p, WarpRows<D, RK, H
   float sc[NR], mx[NR];
 #pragma unroll
   for (int i = 0; i < NR; ++i) {
-    sc[i] = st.c[i] * mt.ks;
+    sc[i] = st.c[i] * ks_scale;
     mx[i] = kNegInf;
   }
 #pragma unroll
@@ -502,7 +627,7 @@ __device__ __forceinline__ void q_tile(const QDecodeParams& p, WarpRows<D, RK, H
   // The scale is >= 0 and rounding monotonic: the scaled maximum is the maximum of
   // the scaled scores.  Each lane checks its own keys; the lanes of a row agree on
   // a new reference only on the few tiles that need one.
-  const float lvs = __log2f(mt.vs);
+  const float lvs = __log2f(vs_scale);
   bool need = false;
 #pragma unroll
   for (int i = 0; i < NR; ++i) {
@@ -553,7 +678,7 @@ __device__ __forceinline__ void q_tile(const QDecodeParams& p, WarpRows<D, RK, H
     f[i] = fast_exp2(mu[i] - (st.w[i] == kNegInf ? 0.f : st.w[i]) + lvs);  // 2^(m - w) sv
   }
   // weights: pz (bf16) for the low-rank product, pv (fp16, scaled) for the values
-  uint32_t pv16[H16 ? NB : 1][4], pz16[H16 ? NB : 1][4], pv8[H8 ? NB : 1][2], pz8[H8 ? NB : 1][2];
+  uint32_t pv16[H16 ? NB : 1][4], pv8[H8 ? NB : 1][2];
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
     if constexpr (H16) {
@@ -584,22 +709,22 @@ __device__ __forceinline__ void q_tile(const QDecodeParams& p, WarpRows<D, RK, H
   // ---- values: O += P V, O^T += V^T P^T
   {
     const int e = lane & 15;  // row of a 16 x 16 block: slots 2t, 2t + 1, 2t + 8, 2t + 9 for rows 4t ..
-    const int key = kw + slot_key(2 * (e >> 2) + (e & 1) + 8 * ((e >> 1) & 1));
+    const uint32_t at = Vs + tile_at<D>(kw + slot_key(2 * (e >> 2) + (e & 1) + 8 * ((e >> 1) & 1)), lane >> 4);
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       uint32_t vm = 0xFFFFFFFFu;  // a lane's four codes belong to four keys
-      if (boundary)
+      if constexpr (LAST)
         vm = (k_lo + 16 * nb < sl ? 0xFFu : 0u) | (k_lo + 16 * nb + 1 < sl ? 0xFF00u : 0u) |
              (k_hi + 16 * nb < sl ? 0xFF0000u : 0u) | (k_hi + 16 * nb + 1 < sl ? 0xFF000000u : 0u);
 #pragma unroll
       for (int cc = 0; cc < KS / 2; ++cc) {
         uint32_t r[4];  // dims 32 cc + 8 x + g8
-        ldsm_b8_x2_t(r[0], r[1], r[2], r[3], Vs + tile_at<D>(key + 16 * nb, 2 * cc + (lane >> 4)));
+        ldsm_b8_x2_t(r[0], r[1], r[2], r[3], (at ^ (cc << 5)) + nb * 16 * D);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t a0, a1, b0, b1;
-          codes_to_half2<FMT>(r[2 * h] & vm, a0, a1);
-          codes_to_half2<FMT>(r[2 * h + 1] & vm, b0, b1);
+          codes_to_half2<FMT>(LAST ? r[2 * h] & vm : r[2 * h], a0, a1);
+          codes_to_half2<FMT>(LAST ? r[2 * h + 1] & vm : r[2 * h + 1], b0, b1);
           if constexpr (H16) {
             float* o = st.o16[4 * cc + 2 * h];
             mma_f16_16816(o, pv16[nb][0], pv16[nb][1], pv16[nb][2], pv16[nb][3], a0, a1);
@@ -611,44 +736,56 @@ __device__ __forceinline__ void q_tile(const QDecodeParams& p, WarpRows<D, RK, H
     }
   }
 
-  // ---- low-rank values: Z += P U_i over each agent's own rows; U rows < a_i or >= seq_len selected out.
-  if (key0 + kQBlock <= a_first) return;
-  const bool one_pass = p.mode == LRKV_BASE_LR_SHARED && !boundary && a_max <= key0;
-  for (int ag = one_pass ? ag_hi : ag_lo; ag <= ag_hi; ++ag) {
-    const int a_i = one_pass ? 0 : a_sm[ag];
-    if (key0 + kQBlock <= a_i) continue;  // this U tile was not loaded
-    const uint32_t ub = Us + (p.mode == LRKV_BASE_SHARED ? ag : 0) * (kQBlock * RK * 2);
-    const bool clean = !boundary && a_i <= key0;
+}
+
+// Low-rank values of the same keys: Z += P U_i over each agent's own rows.  `agents`
+// has a bit for every agent of this warp's rows whose U tile counts here; U rows
+// before a_i or at or past seq_len are selected out (`clean`: there are none).
+template <int D, int RK, int H16, int H8>
+__device__ __forceinline__ void q_low_rank(WarpRows<D, RK, H16, H8>& st, const uint32_t (*pz16)[4],
+                                           const uint32_t (*pz8)[2], uint32_t Us, int slot_bytes, unsigned agents,
+                                           bool one_pass, const int* my_ag, bool clean, const int* a_sm, int key0,
+                                           int kw, int sl) {
+  using WR = WarpRows<D, RK, H16, H8>;
+  constexpr int NB = kQWarpKeys / 16;
+  const int lane = threadIdx.x & 31, t4 = lane & 3, j = lane >> 3;
+  const uint32_t at = Us + u_at<RK>(kw + slot_key((j & 1) * 8 + (lane & 7)), RK == 8 ? 0 : j >> 1);
+  while (agents) {
+    const int ag = __ffs(agents) - 1;
+    agents &= agents - 1;
+    const uint32_t ub = at + ag * slot_bytes;
+    bool use[2 * H16 + H8];
+#pragma unroll
+    for (int i = 0; i < 2 * H16 + H8; ++i) use[i] = one_pass || my_ag[i] == ag;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      const int k16 = key0 + kw + 16 * nb;
-      if (k16 + 16 <= a_i || k16 >= sl) continue;  // warp-uniform
-      uint32_t um_lo = 0xFFFFFFFFu, um_hi = 0xFFFFFFFFu;
-      if (!clean) {
-        const int x = k_lo + 16 * nb, y = k_hi + 16 * nb;
-        um_lo = (x >= a_i && x < sl ? 0xFFFFu : 0u) | (x + 1 >= a_i && x + 1 < sl ? 0xFFFF0000u : 0u);
-        um_hi = (y >= a_i && y < sl ? 0xFFFFu : 0u) | (y + 1 >= a_i && y + 1 < sl ? 0xFFFF0000u : 0u);
-      }
       uint32_t a16[4], b8[2];
       if constexpr (H16) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) a16[i] = one_pass || my_ag[i & 1] == ag ? pz16[nb][i] : 0u;
+        for (int i = 0; i < 4; ++i) a16[i] = use[i & 1] ? pz16[nb][i] : 0u;
       }
       if constexpr (H8) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) b8[i] = one_pass || my_ag[2 * H16] == ag ? pz8[nb][i] : 0u;
+        for (int i = 0; i < 2; ++i) b8[i] = use[2 * H16] ? pz8[nb][i] : 0u;
       }
-      const int j = lane >> 3;
-      const int key = kw + 16 * nb + slot_key((j & 1) * 8 + (lane & 7));
+      uint32_t um_lo = 0xFFFFFFFFu, um_hi = 0xFFFFFFFFu;
+      if (!clean) {
+        const int a_i = one_pass ? 0 : a_sm[ag];
+        const int x = key0 + kw + 16 * nb + 2 * t4, y = key0 + kw + 16 * nb + 8 + ((2 * t4) ^ 4);
+        um_lo = (x >= a_i && x < sl ? 0xFFFFu : 0u) | (x + 1 >= a_i && x + 1 < sl ? 0xFFFF0000u : 0u);
+        um_hi = (y >= a_i && y < sl ? 0xFFFFu : 0u) | (y + 1 >= a_i && y + 1 < sl ? 0xFFFF0000u : 0u);
+      }
 #pragma unroll
       for (int mz = 0; mz < WR::MZ; ++mz) {
         uint32_t r0, r1, r2 = 0, r3 = 0;  // ranks 16 mz + g8: slots 0-7, 8-15; ranks + 8 likewise
-        if constexpr (RK == 8) ldsm_x2_t(r0, r1, ub + u_at<RK>(key, 0));
-        else ldsm_x4_t(r0, r1, r2, r3, ub + u_at<RK>(key, 2 * mz + (j >> 1)));
-        r0 &= um_lo;
-        r1 &= um_hi;
-        r2 &= um_lo;
-        r3 &= um_hi;
+        if constexpr (RK == 8) ldsm_x2_t(r0, r1, ub + nb * 256);
+        else ldsm_x4_t(r0, r1, r2, r3, (ub ^ (mz << 5)) + nb * 32 * RK);
+        if (!clean) {
+          r0 &= um_lo;
+          r1 &= um_hi;
+          r2 &= um_lo;
+          r3 &= um_hi;
+        }
         if constexpr (H16) {
           mma_bf16_16816(st.z16[RK == 8 ? 0 : 2 * mz], a16[0], a16[1], a16[2], a16[3], r0, r1);
           if constexpr (RK > 8) mma_bf16_16816(st.z16[2 * mz + 1], a16[0], a16[1], a16[2], a16[3], r2, r3);
@@ -909,39 +1046,56 @@ __device__ __forceinline__ void finish_item(const QDecodeParams& p, const Range&
   }
 }
 
-template <int FMT, int D, int RK, int H16, int H8, int NRB, int KPW>
-__device__ void q_consumers(const QDecodeParams& p, uint8_t* smem, const QDecodeSmem& lay, uint64_t* full,
-                            uint64_t* empty, volatile int* abort_flag, int* bcast, const Range& range) {
+// Wait until the producer has put tile number n into a stage, then for its bytes.
+__device__ __forceinline__ void q_wait(const QDecodeParams& p, const volatile int* seq, int n, uint64_t* full,
+                                       uint32_t phase, volatile int* abort_flag) {
+  uint32_t spins = 0;
+  while (*seq != n) {
+    if (*abort_flag) break;
+    if (++spins >= p.spin_cap) {
+      *abort_flag = 1;
+      atomicOr(p.flags, LRKV_DEVFLAG_TIMEOUT);
+      break;
+    }
+  }
+  mbar_wait_bounded(full, phase, abort_flag, p.flags, p.spin_cap, true);
+}
+
+template <int FMT, int D, int RK, int H16, int H8, int NRB>
+__device__ void q_consumers(const QDecodeParams& p, uint8_t* smem, const QDecodeSmem& lay, const QBars& bar, int* bcast,
+                            const Range& range) {
   using WR = WarpRows<D, RK, H16, H8>;
   constexpr int RPW = WR::RPW, RP = RPW * NRB, NR = WR::NR;
-  constexpr int KW = kQBlock / KPW;            // warps that share a tile's keys
+  constexpr int KW = kQBlock / kQWarpKeys;     // warps that share a tile's keys
   constexpr int NG = kQWarps / (KW * NRB);     // groups that take tiles in turn
+  constexpr int NB = kQWarpKeys / 16;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2;
   const int rb = warp % NRB, peer = warp / NRB;  // row block; place among the warps that hold its rows
-  const int og = peer / KW, kw = (peer % KW) * KPW;
+  const int og = peer / KW, kw = (peer % KW) * kQWarpKeys;
   float* rec = reinterpret_cast<float*>(smem + lay.rec_off);
   float* mb = reinterpret_cast<float*>(smem + lay.mb_off);
   float* ml = reinterpret_cast<float*>(smem + lay.ml_off);
-  const Meta* meta = reinterpret_cast<const Meta*>(smem + lay.meta_off);
+  uint32_t* qs = reinterpret_cast<uint32_t*>(smem + lay.q_off);
   int* a_sm = reinterpret_cast<int*>(smem + lay.a_off);
   const uint32_t ring = smem_u32(smem);
-  int stage = 0, ntile = 0;
-  uint32_t phase = 0;
+  int stage = 0, ntile = 0, us = 0, un = 0;
+  uint32_t phase = 0, uphase = 0;
   Walk walk;
   walk.start(p, range);
   Seg sg;
   WR st;
   while (walk.next(p, sg)) {
     if (tid < sg.n_ag) a_sm[tid] = load_offset(p, sg.s, sg.i_lo + tid, true);
-    load_queries<D, RK, H16, H8>(p, sg, rb * RPW, st);
+    load_queries<D, RK, H16, H8>(p, sg, rb * RPW, st, qs);
     q_sync();
-    int a_max = 0, a_first = 0x7fffffff;
-    for (int j = 0; j < sg.n_ag; ++j) a_max = max(a_max, a_sm[j]);
+    // this lane's agent's offset (lane j: agent j), and the extremes over the item
+    const int lane_a = lane < sg.n_ag ? a_sm[lane] : 0x7fffffff;
+    const int a_min = __reduce_min_sync(0xFFFFFFFFu, lane_a);
+    const int a_max = __reduce_max_sync(0xFFFFFFFFu, lane < sg.n_ag ? lane_a : 0);
     // agents of this warp's rows, and of the rows whose weights this lane masks
     const int w_lo = sg.row_lo + rb * RPW, w_rows = min(RPW, sg.rows - rb * RPW);
     const int ag_lo = w_rows > 0 ? w_lo / p.G - sg.i_lo : 0;
     const int ag_hi = w_rows > 0 ? (w_lo + w_rows - 1) / p.G - sg.i_lo : -1;
-    for (int ag = ag_lo; ag <= ag_hi; ++ag) a_first = min(a_first, a_sm[ag]);
     int my_ag[2 * H16 + H8];
 #pragma unroll
     for (int i = 0; i < 2 * H16 + H8; ++i) my_ag[i] = 8 * i + g8 < w_rows ? (w_lo + 8 * i + g8) / p.G - sg.i_lo : -1;
@@ -963,24 +1117,53 @@ __device__ void q_consumers(const QDecodeParams& p, uint8_t* smem, const QDecode
       for (int x = 0; x < WR::MZ; ++x) st.z8[x][0] = st.z8[x][1] = st.z8[x][2] = st.z8[x][3] = 0.f;
     }
 
-    const int tiles_hi = sg.sl > 0 ? sg.hi : sg.lo;  // an empty session has no tiles
-    for (int tile = sg.lo; tile < tiles_hi; ++tile) {
-      const bool mine = NG == 1 || ntile % NG == og;
-      const int my_stage = stage;
-      const uint32_t my_phase = phase;
+    QOrder ord;
+    ord.start(sg.nt, sg.lo, p.balance && !range.whole);
+    const int tiles = sg.sl > 0 ? sg.hi - sg.lo : 0;  // an empty session has no tiles
+    for (int k = 0; k < tiles; ++k, ord.next()) {
+      const int key0 = ord.tile() * kQBlock;
+      const int my_n = ntile, my_stage = stage, my_un = un, my_us = us;
+      const uint32_t my_phase = phase, my_uphase = uphase;
+      const bool has_u = key0 + kQBlock > a_min;
       ++ntile;
       if (++stage == p.stages) {
         stage = 0;
         phase ^= 1;
       }
-      if (!mine) continue;
-      mbar_wait_bounded(&full[my_stage], my_phase, abort_flag, p.flags, p.spin_cap, true);
-      const Meta mt = meta[my_stage];
-      if (mt.ok)
-        q_tile<FMT, D, RK, H16, H8, KPW>(p, st, sg, ring + my_stage * lay.stage_bytes, mt, tile * kQBlock, kw, a_sm,
-                                         ag_lo, ag_hi, my_ag, a_first, a_max);
+      if (has_u) {
+        ++un;
+        if (++us == p.u_stages) {
+          us = 0;
+          uphase ^= 1;
+        }
+      }
+      if (NG > 1 && my_n % NG != og) continue;
+      const Meta* meta = bar.meta + my_stage;
+      q_wait(p, &meta->n, my_n, &bar.full[my_stage], my_phase, bar.abort_flag);
+      const float2 scales = *reinterpret_cast<const float2*>(meta);
+      const bool ok = meta->ok != 0;
+      const bool last = key0 + kQBlock > sg.sl;
+      uint32_t pz16[H16 ? NB : 1][4], pz8[H8 ? NB : 1][2];
+      const uint32_t Ks = ring + my_stage * lay.tile_bytes;
+      if (ok) {
+        if (last) q_tile<FMT, D, RK, H16, H8, true>(st, sg.sl, Ks, scales.x, scales.y, key0, kw, qs, pz16, pz8);
+        else q_tile<FMT, D, RK, H16, H8, false>(st, sg.sl, Ks, scales.x, scales.y, key0, kw, qs, pz16, pz8);
+      }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[my_stage]);
+      if (lane == 0) mbar_arrive(&bar.empty[my_stage]);
+      if (has_u) {
+        const uint32_t Us = ring + lay.u_off + my_us * lay.u_bytes;
+        q_wait(p, &bar.useq[my_us], my_un, &bar.u_full[my_us], my_uphase, bar.abort_flag);
+        const bool one_pass = p.mode == LRKV_BASE_LR_SHARED && !last && a_max <= key0;
+        const unsigned mine = __ballot_sync(0xFFFFFFFFu, lane >= ag_lo && lane <= ag_hi && key0 + kQBlock > lane_a);
+        const bool clean = !last && !__any_sync(0xFFFFFFFFu, (mine >> lane & 1) && lane_a > key0);
+        if (ok)
+          q_low_rank<D, RK, H16, H8>(st, pz16, pz8, Us, p.mode == LRKV_BASE_SHARED ? kQBlock * RK * 2 : 0,
+                                     one_pass ? mine & (0u - mine) : mine, one_pass, my_ag, clean, a_sm, key0, kw,
+                                     sg.sl);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.u_empty[my_us]);
+      }
     }
     merge_warps<D, RK, H16, H8, NRB>(st, rec, mb, ml, rb, peer);
     finish_item<D, RK, RP>(p, range, sg, rec, mb, bcast);
@@ -995,25 +1178,37 @@ constexpr int kQBlockThreads = (kQWarps + 4) * 32;
 constexpr int kQConsumerRegs = 224, kQProducerRegs = 56;
 static_assert(kQThreads * kQConsumerRegs + 128 * kQProducerRegs <= kQBlockThreads * 168, "register split");
 
-template <int FMT, int D, int RK, int H16, int H8, int NRB, int KPW>
+template <int FMT, int D, int RK, int H16, int H8, int NRB>
 __global__ void __launch_bounds__(kQBlockThreads, 1)
     decode_quant_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                         const __grid_constant__ CUtensorMap tmU, const QDecodeParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const QDecodeSmem lay = q_smem_plan(D, RK, 16 * H16 + 8 * H8, NRB, p.n_u_slots, p.stages);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + lay.bar_off);
-  uint64_t* empty = full + p.stages;
+  const QDecodeSmem lay = q_smem_plan(D, RK, 16 * H16 + 8 * H8, NRB, p.n_u_slots, p.stages, p.u_stages);
+  QBars bar;
+  bar.full = reinterpret_cast<uint64_t*>(smem + lay.bar_off);
+  bar.empty = bar.full + p.stages;
+  bar.u_full = bar.empty + p.stages;
+  bar.u_empty = bar.u_full + p.u_stages;
+  bar.meta = reinterpret_cast<Meta*>(smem + lay.meta_off);
+  bar.useq = reinterpret_cast<volatile int*>(smem + lay.useq_off);
   Range* range = reinterpret_cast<Range*>(smem + lay.misc_off);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(range + 1);
-  int* bcast = const_cast<int*>(abort_flag) + 1;
+  bar.abort_flag = reinterpret_cast<volatile int*>(range + 1);
+  int* bcast = const_cast<int*>(bar.abort_flag) + 1;
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == kQWarps * 32) {
+    constexpr int READERS = kQBlock / kQWarpKeys * NRB;  // warps that read a tile
     for (int s = 0; s < p.stages; ++s) {
-      mbar_init(&full[s], 2);                           // the tile's bytes; its scales
-      mbar_init(&empty[s], (kQBlock / KPW) * NRB);      // the warps that read the tile
+      mbar_init(&bar.full[s], 2);                        // the tile's bytes; its scales
+      mbar_init(&bar.empty[s], READERS);
+      bar.meta[s].n = -1;
     }
-    *abort_flag = 0;
+    for (int s = 0; s < p.u_stages; ++s) {
+      mbar_init(&bar.u_full[s], 1);
+      mbar_init(&bar.u_empty[s], READERS);
+      bar.useq[s] = -1;
+    }
+    *bar.abort_flag = 0;
     *bcast = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tmK);
@@ -1027,21 +1222,18 @@ __global__ void __launch_bounds__(kQBlockThreads, 1)
   const Range r = *range;
   if (warp >= kQWarps) {
     setmaxnreg_dec<kQProducerRegs>();
-    if (warp == kQWarps)
-      q_producer<D, RK>(p, &tmK, &tmV, &tmU, smem, lay, reinterpret_cast<Meta*>(smem + lay.meta_off), full, empty,
-                        abort_flag, r);
+    if (warp == kQWarps) q_producer<D, RK>(p, &tmK, &tmV, &tmU, smem, lay, bar, r);
   } else {
     setmaxnreg_inc<kQConsumerRegs>();
-    q_consumers<FMT, D, RK, H16, H8, NRB, KPW>(p, smem, lay, full, empty, abort_flag, bcast, r);
+    q_consumers<FMT, D, RK, H16, H8, NRB>(p, smem, lay, bar, bcast, r);
   }
 }
 
 template <int FMT, int D, int RK, int H16, int H8, int NRB>
 lrkv_status launch_q(const QDecodeParams& p, const void* tmK, const void* tmV, const void* tmU, int smem, int ctas,
                      cudaStream_t stream) {
-  constexpr int KPW = 16;
-  auto kern = decode_quant_kernel<FMT, D, RK, H16, H8, NRB, KPW>;
-  if (ensure_dynamic_smem<decode_quant_kernel<FMT, D, RK, H16, H8, NRB, KPW>>(smem) != cudaSuccess) return LRKV_ERR_CUDA;
+  auto kern = decode_quant_kernel<FMT, D, RK, H16, H8, NRB>;
+  if (ensure_dynamic_smem<decode_quant_kernel<FMT, D, RK, H16, H8, NRB>>(smem) != cudaSuccess) return LRKV_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kQBlockThreads);

@@ -64,7 +64,8 @@ struct QDecodeParams {
   int max_seq_len;
   int u_rows;
   int num_pages;
-  int stages;
+  int stages, u_stages;      // ring stages of K/V tiles and of U tiles
+  int balance;               // visit an item's tiles in a low-discrepancy order (QOrder)
   int whole_slack;           // see q_whole_items
   float scale_log2;          // softmax_scale * log2(e)
   float* partials;           // two records per CTA: see q_record_slot
@@ -77,8 +78,9 @@ struct QDecodeParams {
 // Consumer warps of the decode kernel.  A warp holds the query rows of one row
 // block in one of three shapes: up to 8 rows (keys as the MMA's M), up to 16
 // (rows as M), up to 24 (16 + 8).  Items of 25 to 32 rows take two row blocks of
-// 16.  The warps of a row block split a tile's 64 keys.
+// 16.  Two warps of a row block share a tile, 32 keys each.
 constexpr int kQWarps = 8;
+constexpr int kQWarpKeys = 32;
 
 struct QShape {
   int h16, h8, nrb;          // 16-row part, 8-row part, row blocks
@@ -93,20 +95,25 @@ constexpr int kQMergeCols = 32;
 
 // Shared-memory plan (bytes from a 1024-aligned base).
 struct QDecodeSmem {
-  int stage_bytes, rec_off, mb_off, ml_off, meta_off, a_off, bar_off, misc_off, total;
+  int tile_bytes, u_bytes, u_off, rec_off, mb_off, ml_off, q_off, meta_off, a_off, bar_off, useq_off, misc_off, total;
 };
 
-__host__ __device__ inline QDecodeSmem q_smem_plan(int D, int RK, int rows_block, int nrb, int n_u_slots, int stages) {
+__host__ __device__ inline QDecodeSmem q_smem_plan(int D, int RK, int rows_block, int nrb, int n_u_slots, int stages,
+                                                   int u_stages) {
   QDecodeSmem s;
   const int RP = rows_block * nrb;
-  s.stage_bytes = round_up(2 * kQBlock * D + n_u_slots * kQBlock * RK * 2, 1024);
-  s.rec_off = stages * s.stage_bytes;                                    // [m | l | O | Z] of RP rows
+  s.tile_bytes = 2 * kQBlock * D;                                        // K then V of one tile
+  s.u_bytes = n_u_slots * kQBlock * RK * 2;
+  s.u_off = stages * s.tile_bytes;
+  s.rec_off = s.u_off + u_stages * s.u_bytes;                            // [m | l | O | Z] of RP rows
   s.mb_off = s.rec_off + RP * (D + RK + 2) * 4;                          // the warps' columns being merged
   s.ml_off = s.mb_off + kQWarps * rows_block * kQMergeCols * 4;          // the warps' m and l
-  s.meta_off = round_up(s.ml_off + kQWarps * rows_block * 2 * 4, 16);    // {k scale, v scale, ok} of each stage
+  s.q_off = round_up(s.ml_off + kQWarps * rows_block * 2 * 4, 16);       // 24-row blocks: query fragments
+  s.meta_off = s.q_off + (rows_block == 24 ? 24 * D * 2 : 0);            // {k scale, v scale, ok, tile number} of each stage
   s.a_off = s.meta_off + stages * 16;                                    // offsets of the item's agents
   s.bar_off = round_up(s.a_off + kMaxAgents * 4, 16);
-  s.misc_off = s.bar_off + 2 * stages * 8;                               // the CTA's range, abort word, broadcast word
+  s.useq_off = s.bar_off + 2 * (stages + u_stages) * 8;                  // tile number of each U stage
+  s.misc_off = round_up(s.useq_off + u_stages * 4, 16);                  // the CTA's range, abort word, broadcast word
   s.total = s.misc_off + 96;
   return s;
 }

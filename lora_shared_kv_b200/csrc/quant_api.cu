@@ -94,7 +94,7 @@ lrkv_status cache_params(const lrkv_problem* p, const lrkv_kv_view* x, int32_t T
 }
 
 struct QPlan {
-  int G, R, n_rg, rows_per_group, n_u_slots, nt, ctas, stages, smem, RP;
+  int G, R, n_rg, rows_per_group, n_u_slots, nt, ctas, stages, u_stages, smem, RP;
   long long items;
   size_t tickets_off, partials_off, bytes;
 };
@@ -128,16 +128,19 @@ lrkv_status plan_decode_quant(const lrkv_problem* p, int max_seq_len, const Devi
   const lrkv::QShape sh = lrkv::q_shape(pl->rows_per_group);
   const int rows_block = 16 * sh.h16 + 8 * sh.h8;
   pl->RP = rows_block * sh.nrb;
-  // As many stages as fit, up to 12.  With one row block the warps take tiles in
-  // two groups in turn, and an even stage count keeps a stage with one group: a
-  // parity wait can then never be satisfied by an older phase of its stage.
+  // Up to four U stages within 80 KB (one per tile being worked on), then as many
+  // K/V stages as fit, up to 16.
   const int optin = dev.smem_optin > 0 ? dev.smem_optin : 232448;
-  int stages = 12;
-  for (; stages >= 2; stages -= 2)
-    if (lrkv::q_smem_plan(p->head_dim, p->rank, rows_block, sh.nrb, pl->n_u_slots, stages).total + 1024 <= optin) break;
+  const int u_bytes = pl->n_u_slots * LRKV_QUANT_BLOCK * p->rank * 2;
+  pl->u_stages = u_bytes > 81920 / 2 ? 1 : u_bytes * 4 > 81920 ? 81920 / u_bytes : 4;
+  auto smem_of = [&](int stages) {
+    return lrkv::q_smem_plan(p->head_dim, p->rank, rows_block, sh.nrb, pl->n_u_slots, stages, pl->u_stages).total + 1024;
+  };
+  int stages = 16;
+  while (stages >= 2 && smem_of(stages) > optin) --stages;
   if (stages < 2) return fail(LRKV_ERR_UNSUPPORTED, "decode tiles do not fit in shared memory");
   pl->stages = stages;
-  pl->smem = lrkv::q_smem_plan(p->head_dim, p->rank, rows_block, sh.nrb, pl->n_u_slots, stages).total + 1024;
+  pl->smem = smem_of(stages);
   pl->tickets_off = lrkv::kWsHeaderBytes;
   pl->partials_off = pl->tickets_off + ((size_t)pl->items * 4 + 255) / 256 * 256;
   pl->bytes = pl->partials_off + (size_t)2 * pl->ctas * lrkv::q_record_floats(pl->RP, p->head_dim, p->rank) * 4;
@@ -268,6 +271,8 @@ lrkv_status lrkv_attn_decode_quant(const lrkv_problem* p, const void* q, const l
   dp.u_rows = u->num_rows;
   dp.num_pages = kv->page_table ? kv->num_pages : 0;
   dp.stages = pl.stages;
+  dp.u_stages = pl.u_stages;
+  dp.balance = p->mode == LRKV_BASE_SHARED;
   dp.whole_slack = lrkv::kWholeItemSlackTiles;
   dp.scale_log2 = scale_of(p) * 1.4426950408889634f;
   char* ws = static_cast<char*>(workspace);
