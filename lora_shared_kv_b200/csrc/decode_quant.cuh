@@ -928,7 +928,7 @@ __device__ __forceinline__ void finish_item(const QDecodeParams& p, const Range&
   constexpr int E4 = RP * (D + RK) / 4;
   constexpr int PER = (E4 + kQThreads - 1) / kQThreads;
   constexpr int TABLE = kQWarps * (RP > 16 && RP != 24 ? 16 : RP) * kQMergeCols;  // floats of the merge buffer
-  constexpr int CHUNK = TABLE / RP;                                               // records whose scales it holds
+  constexpr int CHUNK = TABLE / RP / 2;                                           // records whose m and l it holds
   const int tid = threadIdx.x;
   const bool shared = !range.whole && (sg.lo > 0 || sg.hi < sg.nt);
   if (shared) {
@@ -948,38 +948,62 @@ __device__ __forceinline__ void finish_item(const QDecodeParams& p, const Range&
     q_sync();
     if (!*bcast) return;
     __threadfence();
-    auto record = [&](int j) {
-      const long long c = c_first + j;
-      return p.partials + q_record_slot(c, c * W / C, sg.item_t0) * REC;
-    };
-    if (tid < RP) {
-      float M = kNegInf;
-      for (int j = 0; j < segs; ++j) M = fmaxf(M, __ldcg(record(j) + tid));
-      rec[tid] = M;
-      rec[RP + tid] = 0.f;
-    }
+    // Only the item's first CTA can hold it in its second record slot.
+    const float* first = p.partials + q_record_slot(c_first, c_first * W / C, sg.item_t0) * REC;
+    const float* rest = p.partials + 2 * (size_t)c_first * REC;
+    auto record = [&](int j) { return j == 0 ? first : rest + (size_t)(2 * j) * REC; };
     float4 acc[PER];
 #pragma unroll
     for (int u = 0; u < PER; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float* t_m = table;                // [CHUNK][RP]: the records' m, then their scales
+    float* t_l = table + CHUNK * RP;   // their l
+    float* corr = rec + 2 * RP;        // what a new maximum does to the sums so far (O's place: free until the end)
+    if (tid < RP) {
+      rec[tid] = kNegInf;
+      rec[RP + tid] = 0.f;
+    }
     for (int j0 = 0; j0 < segs; j0 += CHUNK) {
       const int nj = min(CHUNK, segs - j0);
       q_sync();
       for (int e = tid; e < nj * RP; e += kQThreads) {
-        const float mj = __ldcg(record(j0 + e / RP) + e % RP);
-        table[e] = mj == kNegInf ? 0.f : fast_exp2(mj - rec[e % RP]);
+        const float* r = record(j0 + e / RP) + e % RP;
+        t_m[e] = __ldcg(r);
+        t_l[e] = __ldcg(r + RP);
       }
       q_sync();
       if (tid < RP) {
-        float L = rec[RP + tid];
-        for (int j = 0; j < nj; ++j) L += __ldcg(record(j0 + j) + RP + tid) * table[j * RP + tid];
-        rec[RP + tid] = L;
+        const float before = rec[tid];
+        float M = before, L = 0.f;
+        for (int j = 0; j < nj; ++j) M = fmaxf(M, t_m[j * RP + tid]);
+        for (int j = 0; j < nj; ++j) {
+          const float mj = t_m[j * RP + tid];
+          const float sc = mj == kNegInf ? 0.f : fast_exp2(mj - M);
+          t_m[j * RP + tid] = sc;
+          L += sc == 0.f ? 0.f : t_l[j * RP + tid] * sc;
+        }
+        const float c = before == kNegInf ? 0.f : fast_exp2(before - M);
+        rec[tid] = M;
+        rec[RP + tid] = rec[RP + tid] * c + L;
+        corr[tid] = c;
+      }
+      q_sync();
+      if (j0 > 0) {
+#pragma unroll
+        for (int u = 0; u < PER; ++u) {
+          const int e = 4 * (tid + u * kQThreads);
+          if (e >= 4 * E4) continue;
+          const float c = corr[e < RP * D ? e / D : (e - RP * D) / RK];
+          acc[u].x *= c;
+          acc[u].y *= c;
+          acc[u].z *= c;
+          acc[u].w *= c;
+        }
       }
       for (int jb = 0; jb < nj; jb += kMergeBatch) {
         float4 v[kMergeBatch][PER];
 #pragma unroll
         for (int q = 0; q < kMergeBatch; ++q) {
-          if (jb + q >= nj) break;
-          const float4* src = reinterpret_cast<const float4*>(record(j0 + jb + q) + 2 * RP);
+          const float4* src = reinterpret_cast<const float4*>(record(j0 + min(jb + q, nj - 1)) + 2 * RP);
 #pragma unroll
           for (int u = 0; u < PER; ++u)
             if (tid + u * kQThreads < E4) v[q][u] = __ldcg(src + tid + u * kQThreads);
@@ -991,7 +1015,7 @@ __device__ __forceinline__ void finish_item(const QDecodeParams& p, const Range&
           for (int u = 0; u < PER; ++u) {
             const int e = 4 * (tid + u * kQThreads);
             if (e >= 4 * E4) continue;
-            const float sc = table[(jb + q) * RP + (e < RP * D ? e / D : (e - RP * D) / RK)];
+            const float sc = t_m[(jb + q) * RP + (e < RP * D ? e / D : (e - RP * D) / RK)];
             acc[u].x += v[q][u].x * sc;
             acc[u].y += v[q][u].y * sc;
             acc[u].z += v[q][u].z * sc;
@@ -1000,6 +1024,7 @@ __device__ __forceinline__ void finish_item(const QDecodeParams& p, const Range&
         }
       }
     }
+    q_sync();  // corr has been read
 #pragma unroll
     for (int u = 0; u < PER; ++u) {
       const int e4 = tid + u * kQThreads;
