@@ -60,12 +60,17 @@ struct Range {
   int pad;
 };
 
-// Stage facts that do not come through the tile copies.  `n` is the number of the
-// tile in the stage: a consumer waits for its own there before it waits on the
-// stage's mbarrier, so that a parity wait is never satisfied by an older phase.
-struct Meta {
-  float ks, vs;
-  int ok, n;
+// What the producer tells of the tile in a stage.  `n` is its number among the
+// CTA's tiles: a consumer waits for its own there before it waits on the stage's
+// mbarrier, so that a parity wait is never satisfied by an older phase.
+struct __align__(16) Meta {
+  float ks, vs;  // the block's scales
+  int n;
+  int key0;      // the tile's first key; -1: not copied (a bad page id)
+  int us;        // U stage, -1: the tile needs none
+  int un;        // number of the U tile among the CTA's
+  int uphase;
+  int pad;
 };
 
 __device__ __forceinline__ int clamp_len(const QDecodeParams& p, int sl) {
@@ -308,7 +313,10 @@ __device__ void q_producer(const QDecodeParams& p, const CUtensorMap* tmK, const
       if (lane == 0) {
         uint64_t* full = &bar.full[stage];
         Meta* meta = &bar.meta[stage];
-        meta->ok = ok;
+        meta->key0 = ok ? tile * kQBlock : -1;
+        meta->us = need ? us : -1;
+        meta->un = un;
+        meta->uphase = uphase;
         *reinterpret_cast<volatile int*>(&meta->n) = n;
         if (!ok) {
           atomicOr(p.flags, LRKV_DEVFLAG_PAGE);
@@ -1103,8 +1111,9 @@ __device__ void q_consumers(const QDecodeParams& p, uint8_t* smem, const QDecode
   uint32_t* qs = reinterpret_cast<uint32_t*>(smem + lay.q_off);
   int* a_sm = reinterpret_cast<int*>(smem + lay.a_off);
   const uint32_t ring = smem_u32(smem);
-  int stage = 0, ntile = 0, us = 0, un = 0;
-  uint32_t phase = 0, uphase = 0;
+  // the group's next tile (number, stage, phase); the CTA's tiles before this segment
+  int n = og, stage = og % p.stages, before = 0;
+  uint32_t phase = (og / p.stages) & 1;
   Walk walk;
   walk.start(p, range);
   Seg sg;
@@ -1113,9 +1122,8 @@ __device__ void q_consumers(const QDecodeParams& p, uint8_t* smem, const QDecode
     if (tid < sg.n_ag) a_sm[tid] = load_offset(p, sg.s, sg.i_lo + tid, true);
     load_queries<D, RK, H16, H8>(p, sg, rb * RPW, st, qs);
     q_sync();
-    // this lane's agent's offset (lane j: agent j), and the extremes over the item
+    // this lane's agent's offset (lane j: agent j), and the item's largest
     const int lane_a = lane < sg.n_ag ? a_sm[lane] : 0x7fffffff;
-    const int a_min = __reduce_min_sync(0xFFFFFFFFu, lane_a);
     const int a_max = __reduce_max_sync(0xFFFFFFFFu, lane < sg.n_ag ? lane_a : 0);
     // agents of this warp's rows, and of the rows whose weights this lane masks
     const int w_lo = sg.row_lo + rb * RPW, w_rows = min(RPW, sg.rows - rb * RPW);
@@ -1142,52 +1150,40 @@ __device__ void q_consumers(const QDecodeParams& p, uint8_t* smem, const QDecode
       for (int x = 0; x < WR::MZ; ++x) st.z8[x][0] = st.z8[x][1] = st.z8[x][2] = st.z8[x][3] = 0.f;
     }
 
-    QOrder ord;
-    ord.start(sg.nt, sg.lo, p.balance && !range.whole);
-    const int tiles = sg.sl > 0 ? sg.hi - sg.lo : 0;  // an empty session has no tiles
-    for (int k = 0; k < tiles; ++k, ord.next()) {
-      const int key0 = ord.tile() * kQBlock;
-      const int my_n = ntile, my_stage = stage, my_un = un, my_us = us;
-      const uint32_t my_phase = phase, my_uphase = uphase;
-      const bool has_u = key0 + kQBlock > a_min;
-      ++ntile;
-      if (++stage == p.stages) {
-        stage = 0;
-        phase ^= 1;
-      }
-      if (has_u) {
-        ++un;
-        if (++us == p.u_stages) {
-          us = 0;
-          uphase ^= 1;
-        }
-      }
-      if (NG > 1 && my_n % NG != og) continue;
-      const Meta* meta = bar.meta + my_stage;
-      q_wait(p, &meta->n, my_n, &bar.full[my_stage], my_phase, bar.abort_flag);
+    before += sg.sl > 0 ? sg.hi - sg.lo : 0;  // an empty session has no tiles
+    while (n < before) {
+      const Meta* meta = bar.meta + stage;
+      q_wait(p, &meta->n, n, &bar.full[stage], phase, bar.abort_flag);
       const float2 scales = *reinterpret_cast<const float2*>(meta);
-      const bool ok = meta->ok != 0;
+      const int key0 = meta->key0, us = meta->us;
       const bool last = key0 + kQBlock > sg.sl;
       uint32_t pz16[H16 ? NB : 1][4], pz8[H8 ? NB : 1][2];
-      const uint32_t Ks = ring + my_stage * lay.tile_bytes;
-      if (ok) {
+      const uint32_t Ks = ring + stage * lay.tile_bytes;
+      if (key0 >= 0) {
         if (last) q_tile<FMT, D, RK, H16, H8, true>(st, sg.sl, Ks, scales.x, scales.y, key0, kw, qs, pz16, pz8);
         else q_tile<FMT, D, RK, H16, H8, false>(st, sg.sl, Ks, scales.x, scales.y, key0, kw, qs, pz16, pz8);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.empty[my_stage]);
-      if (has_u) {
-        const uint32_t Us = ring + lay.u_off + my_us * lay.u_bytes;
-        q_wait(p, &bar.useq[my_us], my_un, &bar.u_full[my_us], my_uphase, bar.abort_flag);
-        const bool one_pass = p.mode == LRKV_BASE_LR_SHARED && !last && a_max <= key0;
-        const unsigned mine = __ballot_sync(0xFFFFFFFFu, lane >= ag_lo && lane <= ag_hi && key0 + kQBlock > lane_a);
-        const bool clean = !last && !__any_sync(0xFFFFFFFFu, (mine >> lane & 1) && lane_a > key0);
-        if (ok)
-          q_low_rank<D, RK, H16, H8>(st, pz16, pz8, Us, p.mode == LRKV_BASE_SHARED ? kQBlock * RK * 2 : 0,
+      if (us >= 0) {
+        q_wait(p, &bar.useq[us], meta->un, &bar.u_full[us], meta->uphase, bar.abort_flag);
+        if (key0 >= 0) {
+          const bool one_pass = p.mode == LRKV_BASE_LR_SHARED && !last && a_max <= key0;
+          const unsigned mine = __ballot_sync(0xFFFFFFFFu, lane >= ag_lo && lane <= ag_hi && key0 + kQBlock > lane_a);
+          const bool clean = !last && !__any_sync(0xFFFFFFFFu, (mine >> lane & 1) && lane_a > key0);
+          q_low_rank<D, RK, H16, H8>(st, pz16, pz8, ring + lay.u_off + us * lay.u_bytes,
+                                     p.mode == LRKV_BASE_SHARED ? kQBlock * RK * 2 : 0,
                                      one_pass ? mine & (0u - mine) : mine, one_pass, my_ag, clean, a_sm, key0, kw,
                                      sg.sl);
+        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.u_empty[my_us]);
+        if (lane == 0) mbar_arrive(&bar.u_empty[us]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.empty[stage]);
+      n += NG;
+      stage += NG;
+      while (stage >= p.stages) {
+        stage -= p.stages;
+        phase ^= 1;
       }
     }
     merge_warps<D, RK, H16, H8, NRB>(st, rec, mb, ml, rb, peer);

@@ -109,8 +109,8 @@ __host__ __device__ inline QDecodeSmem q_smem_plan(int D, int RK, int rows_block
   s.mb_off = s.rec_off + RP * (D + RK + 2) * 4;                          // the warps' columns being merged
   s.ml_off = s.mb_off + kQWarps * rows_block * kQMergeCols * 4;          // the warps' m and l
   s.q_off = round_up(s.ml_off + kQWarps * rows_block * 2 * 4, 16);       // 24-row blocks: query fragments
-  s.meta_off = s.q_off + (rows_block == 24 ? 24 * D * 2 : 0);            // {k scale, v scale, ok, tile number} of each stage
-  s.a_off = s.meta_off + stages * 16;                                    // offsets of the item's agents
+  s.meta_off = s.q_off + (rows_block == 24 ? 24 * D * 2 : 0);            // what the producer tells of each stage
+  s.a_off = s.meta_off + stages * 32;                                    // offsets of the item's agents
   s.bar_off = round_up(s.a_off + kMaxAgents * 4, 16);
   s.useq_off = s.bar_off + 2 * (stages + u_stages) * 8;                  // tile number of each U stage
   s.misc_off = round_up(s.useq_off + u_stages * 4, 16);                  // the CTA's range, abort word, broadcast word
