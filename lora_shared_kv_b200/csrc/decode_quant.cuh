@@ -60,9 +60,10 @@ struct Range {
   int pad;
 };
 
-// What the producer tells of the tile in a stage.  `n` is its number among the
-// CTA's tiles: a consumer waits for its own there before it waits on the stage's
-// mbarrier, so that a parity wait is never satisfied by an older phase.
+// What the meta warp tells of the tile in a stage.  `n`, written last, is its number
+// among the CTA's tiles: a consumer waits for its own there before it reads the rest
+// and before it waits on the stage's mbarrier, so that a parity wait is never
+// satisfied by an older phase.
 struct __align__(16) Meta {
   float ks, vs;  // the block's scales
   int n;
@@ -259,78 +260,93 @@ __device__ __forceinline__ int load_offset(const QDecodeParams& p, int s, int ag
 }
 
 // ---------------------------------------------------------------------------
-// producer warp
+// producer warps
 // ---------------------------------------------------------------------------
-// Tile n of the CTA goes to ring stage n % stages.  A stage is full after two
-// arrivals: the bytes of the K/V copies, and the two scales' 4-byte copies.  Tiles
-// that reach past an offset take a stage of the U ring too; tiles without one then
-// do not hold its space.
+// Tile n of the CTA goes to ring stage n % stages.  Tiles that reach past an offset
+// take a stage of the U ring too; tiles without one then do not hold its space.
+// Three warps produce, each walking the CTA's tiles by itself: one issues the K/V
+// copies, one the U copies, one writes the stages' Meta (a single warp doing it all
+// took 1,400 cycles a tile, twice what a tile takes at the HBM rate).
 struct QBars {
   uint64_t *full, *empty, *u_full, *u_empty;
   Meta* meta;
-  volatile int* useq;
+  int* useq;
   volatile int* abort_flag;
 };
 
-template <int D, int RK>
-__device__ void q_producer(const QDecodeParams& p, const CUtensorMap* tmK, const CUtensorMap* tmV,
-                           const CUtensorMap* tmU, uint8_t* smem, const QDecodeSmem& lay, const QBars& bar,
-                           const Range& range) {
+__device__ __forceinline__ void st_release(int* p, int v) {
+  asm volatile("st.release.cta.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(p)), "r"(v) : "memory");
+}
+__device__ __forceinline__ int ld_acquire(const int* p) {
+  int v;
+  asm volatile("ld.acquire.cta.shared::cta.b32 %0, [%1];" : "=r"(v) : "r"(smem_u32(p)) : "memory");
+  return v;
+}
+
+// Wait until a stage is free.  False after an abort: the consumers then release stages
+// without waiting for their copies, so nothing more may be issued.  Warp-uniform.
+__device__ __forceinline__ bool q_wait_free(const QDecodeParams& p, uint64_t* empty, uint32_t phase,
+                                            volatile int* abort_flag) {
+  const bool freed = mbar_wait_bounded(empty, phase ^ 1, abort_flag, p.flags, p.spin_cap, true);
+  return !__any_sync(0xFFFFFFFFu, !freed || *abort_flag);
+}
+
+// After an abort: wait (bounded) for the copies of the last `issued` stages to land.
+__device__ __forceinline__ void q_drain(uint64_t* full, int stages, int issued, int stage, uint32_t phase) {
+  for (int j = 0; j < (issued < stages ? issued : stages); ++j) {
+    if (--stage < 0) {
+      stage = stages - 1;
+      phase ^= 1;
+    }
+    uint32_t spins = 0;
+    while (!mbar_try_wait(&full[stage], phase) && ++spins < kSpinCap) {
+    }
+  }
+}
+
+template <int D>
+__device__ void q_produce_kv(const QDecodeParams& p, const CUtensorMap* tmK, const CUtensorMap* tmV, uint8_t* smem,
+                             const QDecodeSmem& lay, const QBars& bar, const Range& range) {
   const int lane = threadIdx.x & 31;
-  const uint64_t pol_kv = policy_evict_first();
-  const uint64_t pol_u = policy_evict_last();
+  const uint64_t policy = policy_evict_first();
   constexpr int KV_BYTES = kQBlock * D;
-  constexpr int U_BYTES = kQBlock * RK * 2;
   const bool paged = p.page_table != nullptr;
-  int stage = 0, n = 0, us = 0, un = 0;
-  uint32_t phase = 0, uphase = 0;
+  int stage = 0, n = 0;
+  uint32_t phase = 0;
   bool stop = p.stall != 0;  // the test hook: issue nothing, so the consumers' waits run out
   Walk walk;
   walk.start(p, range);
   Seg sg;
   while (!stop && walk.next(p, sg)) {
     if (sg.sl == 0) continue;
-    const int my_a = lane < sg.n_ag ? load_offset(p, sg.s, sg.i_lo + lane, false) : 0x7fffffff;
-    int ids = 0;
+    const int tiles = sg.hi - sg.lo;
     QOrder ord;
     ord.start(sg.nt, sg.lo, p.balance && !range.whole);
-    for (int k = 0; k < sg.hi - sg.lo; ++k, ord.next()) {
+    // page ids of 32 tiles, one per lane, and of the 32 after them
+    const int32_t* table = p.page_table + (size_t)sg.s * p.pt_stride;
+    int ids = paged && lane < tiles ? __ldg(table + ord.ahead(lane)) : 0, ids_next = 0;
+    for (int k = 0; k < tiles; ++k, ord.next()) {
+      if (paged && (k & 31) == 0) {
+        if (k > 0) ids = ids_next;
+        ids_next = k + 32 + lane < tiles ? __ldg(table + ord.ahead(32 + lane)) : 0;
+      }
       const int tile = ord.tile();
-      if (paged && (k & 31) == 0)  // page ids of the next 32 tiles, one per lane
-        ids = k + lane < sg.hi - sg.lo ? __ldg(p.page_table + (size_t)sg.s * p.pt_stride + ord.ahead(lane)) : 0;
-      const int page = paged ? __shfl_sync(0xFFFFFFFFu, ids, k & 31) : 0;
-      const unsigned need = __ballot_sync(0xFFFFFFFFu, lane < sg.n_ag && (tile + 1) * kQBlock > my_a);
-      const bool ok = !paged || (page >= 0 && page < p.num_pages);
-      bool freed = mbar_wait_bounded(&bar.empty[stage], phase ^ 1, bar.abort_flag, p.flags, p.spin_cap, true);
-      // After an abort the consumers release stages without waiting for their
-      // copies, so nothing more may be issued; the whole warp leaves together.
-      if (__any_sync(0xFFFFFFFFu, !freed || *bar.abort_flag)) {
+      const int page = __shfl_sync(0xFFFFFFFFu, ids, k & 31);
+      if (!q_wait_free(p, &bar.empty[stage], phase, bar.abort_flag)) {
         stop = true;
         break;
       }
-      const long long sc = paged ? page * p.s_sp + sg.g * p.s_sh : sg.s * p.s_ss + sg.g * p.s_sh + tile;
-      const int c3 = paged ? page : sg.s;
       if (lane == 0) {
         uint64_t* full = &bar.full[stage];
-        Meta* meta = &bar.meta[stage];
-        meta->key0 = ok ? tile * kQBlock : -1;
-        meta->us = need ? us : -1;
-        meta->un = un;
-        meta->uphase = uphase;
-        *reinterpret_cast<volatile int*>(&meta->n) = n;
-        if (!ok) {
+        if (paged && (page < 0 || page >= p.num_pages)) {
           atomicOr(p.flags, LRKV_DEVFLAG_PAGE);
           mbar_arrive(full);
-          mbar_arrive(full);
         } else {
-          uint8_t* st = smem + (size_t)stage * lay.tile_bytes;
-          const int c1 = paged ? 0 : tile * kQBlock;
+          uint8_t* st = smem + stage * lay.tile_bytes;
+          const int c1 = paged ? 0 : tile * kQBlock, c3 = paged ? page : sg.s;
           mbar_arrive_expect_tx(full, 2 * KV_BYTES);
-          tma_load_4d(st, tmK, full, 0, c1, sg.g, c3, pol_kv);
-          tma_load_4d(st + KV_BYTES, tmV, full, 0, c1, sg.g, c3, pol_kv);
-          cp_async4(smem_u32(&meta->ks), p.k_scale + sc);
-          cp_async4(smem_u32(&meta->vs), p.v_scale + sc);
-          cp_async_mbar_arrive(full);
+          tma_load_4d(st, tmK, full, 0, c1, sg.g, c3, policy);
+          tma_load_4d(st + KV_BYTES, tmV, full, 0, c1, sg.g, c3, policy);
         }
       }
       __syncwarp();
@@ -339,52 +355,130 @@ __device__ void q_producer(const QDecodeParams& p, const CUtensorMap* tmK, const
         stage = 0;
         phase ^= 1;
       }
-      if (need) {
-        freed = mbar_wait_bounded(&bar.u_empty[us], uphase ^ 1, bar.abort_flag, p.flags, p.spin_cap, true);
-        if (__any_sync(0xFFFFFFFFu, !freed || *bar.abort_flag)) {
-          stop = true;
-          break;
+    }
+  }
+  // no copy of this CTA may still be landing in shared memory when it exits
+  if (*bar.abort_flag && lane == 0) q_drain(bar.full, p.stages, n, stage, phase);
+}
+
+template <int RK>
+__device__ void q_produce_u(const QDecodeParams& p, const CUtensorMap* tmU, uint8_t* smem, const QDecodeSmem& lay,
+                            const QBars& bar, const Range& range) {
+  const int lane = threadIdx.x & 31;
+  const uint64_t policy = policy_evict_last();
+  constexpr int U_BYTES = kQBlock * RK * 2;
+  const bool per_agent = p.mode == LRKV_BASE_SHARED;
+  int us = 0, un = 0;
+  uint32_t phase = 0;
+  bool stop = p.stall != 0;
+  Walk walk;
+  walk.start(p, range);
+  Seg sg;
+  while (!stop && walk.next(p, sg)) {
+    if (sg.sl == 0) continue;
+    const int my_a = lane < sg.n_ag ? load_offset(p, sg.s, sg.i_lo + lane, false) : 0x7fffffff;
+    QOrder ord;
+    ord.start(sg.nt, sg.lo, p.balance && !range.whole);
+    for (int k = 0; k < sg.hi - sg.lo; ++k, ord.next()) {
+      const int key0 = ord.tile() * kQBlock;
+      const unsigned need = __ballot_sync(0xFFFFFFFFu, key0 + kQBlock > my_a);
+      if (!need) continue;
+      if (!q_wait_free(p, &bar.u_empty[us], phase, bar.abort_flag)) {
+        stop = true;
+        break;
+      }
+      uint64_t* full = &bar.u_full[us];
+      if (lane == 0) {
+        st_release(&bar.useq[us], un);
+        mbar_arrive_expect_tx(full, (per_agent ? __popc(need) : 1) * U_BYTES);
+      }
+      __syncwarp();
+      if (per_agent ? (need >> lane & 1) : lane == 0)  // one agent's tile per lane
+        tma_load_4d(smem + lay.u_off + us * lay.u_bytes + lane * U_BYTES, tmU, full, 0, key0,
+                    per_agent ? sg.i_lo + lane : 0, sg.s, policy);
+      ++un;
+      if (++us == p.u_stages) {
+        us = 0;
+        phase ^= 1;
+      }
+    }
+  }
+  __syncwarp();
+  if (*bar.abort_flag && lane == 0) q_drain(bar.u_full, p.u_stages, un, us, phase);
+}
+
+__device__ __forceinline__ void q_produce_meta(const QDecodeParams& p, const QBars& bar, const Range& range) {
+  const int lane = threadIdx.x & 31;
+  const bool paged = p.page_table != nullptr;
+  int stage = 0, n = 0, us = 0, un = 0;
+  uint32_t phase = 0, uphase = 0;
+  bool stop = p.stall != 0;
+  Walk walk;
+  walk.start(p, range);
+  Seg sg;
+  while (!stop && walk.next(p, sg)) {
+    if (sg.sl == 0) continue;
+    const int tiles = sg.hi - sg.lo;
+    const int my_a = lane < sg.n_ag ? load_offset(p, sg.s, sg.i_lo + lane, false) : 0x7fffffff;
+    const int a_min = __reduce_min_sync(0xFFFFFFFFu, my_a);
+    QOrder ord;
+    ord.start(sg.nt, sg.lo, p.balance && !range.whole);
+    const int32_t* table = p.page_table + (size_t)sg.s * p.pt_stride;
+    const long long dense = sg.s * p.s_ss + sg.g * p.s_sh, head = sg.g * p.s_sh;
+    // one lane per tile of a run of 32: its place in the cache (page, or tile), its
+    // scales; the next run's are fetched while this one is written
+    auto fetch = [&](int where, float& ks, float& vs) {
+      const bool ok = where >= 0 && (!paged || where < p.num_pages);
+      const long long at = paged ? where * p.s_sp + head : dense + where;
+      ks = ok ? __ldg(p.k_scale + at) : 0.f;
+      vs = ok ? __ldg(p.v_scale + at) : 0.f;
+      return ok;
+    };
+    int where = lane < tiles ? (paged ? __ldg(table + ord.ahead(lane)) : ord.ahead(lane)) : -1, where_next = -1;
+    float ks, vs, ks_next = 0.f, vs_next = 0.f;
+    bool ok = fetch(where, ks, vs), ok_next = false;
+    for (int k = 0; k < tiles; ++k, ord.next()) {
+      const int in = k & 31;
+      if (in == 0) {
+        if (k > 0) {
+          ks = ks_next;
+          vs = vs_next;
+          ok = ok_next;
         }
-        if (lane == 0) {
-          uint64_t* full = &bar.u_full[us];
-          unsigned m = !ok ? 0u : p.mode == LRKV_BASE_SHARED ? need : 1u;
-          bar.useq[us] = un;
-          if (m) mbar_arrive_expect_tx(full, __popc(m) * U_BYTES);
-          else mbar_arrive(full);
-          while (m) {
-            const int slot = __ffs(m) - 1;
-            m &= m - 1;
-            tma_load_4d(smem + lay.u_off + us * lay.u_bytes + slot * U_BYTES, tmU, full, 0, tile * kQBlock,
-                        p.mode == LRKV_BASE_SHARED ? sg.i_lo + slot : 0, sg.s, pol_u);
-          }
-        }
-        __syncwarp();
+        const int ahead = ord.ahead(32 + lane);
+        where_next = k + 32 + lane < tiles ? (paged ? __ldg(table + ahead) : ahead) : -1;
+      } else if (in == 16) {
+        ok_next = fetch(where_next, ks_next, vs_next);
+      }
+      const int key0 = ord.tile() * kQBlock;
+      const bool has_u = key0 + kQBlock > a_min;
+      if (!q_wait_free(p, &bar.empty[stage], phase, bar.abort_flag)) {
+        stop = true;
+        break;
+      }
+      if (lane == in) {
+        Meta* m = &bar.meta[stage];
+        m->ks = ks;
+        m->vs = vs;
+        m->key0 = ok ? key0 : -1;
+        m->us = has_u ? us : -1;
+        m->un = un;
+        m->uphase = uphase;
+        st_release(&m->n, n);
+      }
+      __syncwarp();
+      ++n;
+      if (++stage == p.stages) {
+        stage = 0;
+        phase ^= 1;
+      }
+      if (has_u) {
         ++un;
         if (++us == p.u_stages) {
           us = 0;
           uphase ^= 1;
         }
       }
-    }
-  }
-  // After an abort the consumers may stop waiting; no copy of this CTA may still
-  // be landing in shared memory when it exits.
-  if (lane == 0) {
-    cp_async_wait<0>();
-    if (*bar.abort_flag) {
-      auto drain = [](uint64_t* full, int stages, int issued, int st, uint32_t ph) {
-        for (int j = 0; j < (issued < stages ? issued : stages); ++j) {
-          if (--st < 0) {
-            st = stages - 1;
-            ph ^= 1;
-          }
-          uint32_t spins = 0;
-          while (!mbar_try_wait(&full[st], ph) && ++spins < kSpinCap) {
-          }
-        }
-      };
-      drain(bar.full, p.stages, n, stage, phase);
-      drain(bar.u_full, p.u_stages, un, us, uphase);
     }
   }
 }
@@ -1079,11 +1173,11 @@ __device__ __forceinline__ void finish_item(const QDecodeParams& p, const Range&
   }
 }
 
-// Wait until the producer has put tile number n into a stage, then for its bytes.
-__device__ __forceinline__ void q_wait(const QDecodeParams& p, const volatile int* seq, int n, uint64_t* full,
-                                       uint32_t phase, volatile int* abort_flag) {
+// Wait until a stage belongs to tile number n, then for its bytes.
+__device__ __forceinline__ void q_wait(const QDecodeParams& p, const int* seq, int n, uint64_t* full, uint32_t phase,
+                                       volatile int* abort_flag) {
   uint32_t spins = 0;
-  while (*seq != n) {
+  while (ld_acquire(seq) != n) {
     if (*abort_flag) break;
     if (++spins >= p.spin_cap) {
       *abort_flag = 1;
@@ -1192,7 +1286,7 @@ __device__ void q_consumers(const QDecodeParams& p, uint8_t* smem, const QDecode
   }
 }
 
-// Three warpgroups: two of consumers, one whose first warp produces.  A thread is
+// Three warpgroups: two of consumers, one of producers.  A thread is
 // launched with 168 registers (65536 / 384); the producers' share goes to the
 // consumers: 2 x 128 x 224 + 128 x 56 = 384 x 168.
 constexpr int kQBlockThreads = (kQWarps + 4) * 32;
@@ -1212,7 +1306,7 @@ __global__ void __launch_bounds__(kQBlockThreads, 1)
   bar.u_full = bar.empty + p.stages;
   bar.u_empty = bar.u_full + p.u_stages;
   bar.meta = reinterpret_cast<Meta*>(smem + lay.meta_off);
-  bar.useq = reinterpret_cast<volatile int*>(smem + lay.useq_off);
+  bar.useq = reinterpret_cast<int*>(smem + lay.useq_off);
   Range* range = reinterpret_cast<Range*>(smem + lay.misc_off);
   bar.abort_flag = reinterpret_cast<volatile int*>(range + 1);
   int* bcast = const_cast<int*>(bar.abort_flag) + 1;
@@ -1220,7 +1314,7 @@ __global__ void __launch_bounds__(kQBlockThreads, 1)
   if (threadIdx.x == kQWarps * 32) {
     constexpr int READERS = kQBlock / kQWarpKeys * NRB;  // warps that read a tile
     for (int s = 0; s < p.stages; ++s) {
-      mbar_init(&bar.full[s], 2);                        // the tile's bytes; its scales
+      mbar_init(&bar.full[s], 1);
       mbar_init(&bar.empty[s], READERS);
       bar.meta[s].n = -1;
     }
@@ -1243,7 +1337,9 @@ __global__ void __launch_bounds__(kQBlockThreads, 1)
   const Range r = *range;
   if (warp >= kQWarps) {
     setmaxnreg_dec<kQProducerRegs>();
-    if (warp == kQWarps) q_producer<D, RK>(p, &tmK, &tmV, &tmU, smem, lay, bar, r);
+    if (warp == kQWarps) q_produce_kv<D>(p, &tmK, &tmV, smem, lay, bar, r);
+    else if (warp == kQWarps + 1) q_produce_u<RK>(p, &tmU, smem, lay, bar, r);
+    else if (warp == kQWarps + 2) q_produce_meta(p, bar, r);
   } else {
     setmaxnreg_inc<kQConsumerRegs>();
     q_consumers<FMT, D, RK, H16, H8, NRB>(p, smem, lay, bar, bcast, r);

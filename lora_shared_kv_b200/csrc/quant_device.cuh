@@ -63,14 +63,4 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
-// A 4-byte copy from global to shared memory whose completion an mbarrier can track.
-__device__ __forceinline__ void cp_async4(uint32_t smem_dst, const void* gmem_src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_dst), "l"(gmem_src) : "memory");
-}
-// One arrival on `bar` once this thread's copies issued so far have landed (the
-// barrier's count includes it).
-__device__ __forceinline__ void cp_async_mbar_arrive(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
 }  // namespace lrkv
