@@ -60,18 +60,14 @@ struct Range {
   int pad;
 };
 
-// What the meta warp tells of the tile in a stage.  `n`, written last, is its number
-// among the CTA's tiles: a consumer waits for its own there before it reads the rest
-// and before it waits on the stage's mbarrier, so that a parity wait is never
-// satisfied by an older phase.
+// What the meta warp tells of the tile in a stage.
 struct __align__(16) Meta {
   float ks, vs;  // the block's scales
-  int n;
   int key0;      // the tile's first key; -1: not copied (a bad page id)
   int us;        // U stage, -1: the tile needs none
   int un;        // number of the U tile among the CTA's
   int uphase;
-  int pad;
+  int pad[2];
 };
 
 __device__ __forceinline__ int clamp_len(const QDecodeParams& p, int sl) {
@@ -267,21 +263,17 @@ __device__ __forceinline__ int load_offset(const QDecodeParams& p, int s, int ag
 // Three warps produce, each walking the CTA's tiles by itself: one issues the K/V
 // copies, one the U copies, one writes the stages' Meta (a single warp doing it all
 // took 1,400 cycles a tile, twice what a tile takes at the HBM rate).
+// The stages of the K/V ring are a multiple of the consumer groups, so a stage always
+// serves one group, which has seen every earlier phase of its barriers.  A U stage
+// serves any group: useq holds the number of its U tile, and a group waits for its own
+// number there before it waits on the barrier, lest an older phase of the same parity
+// satisfy the wait.
 struct QBars {
-  uint64_t *full, *empty, *u_full, *u_empty;
+  uint64_t *full, *empty, *told, *u_full, *u_empty;  // told: the stage's Meta is written
   Meta* meta;
-  int* useq;
+  volatile int* useq;
   volatile int* abort_flag;
 };
-
-__device__ __forceinline__ void st_release(int* p, int v) {
-  asm volatile("st.release.cta.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(p)), "r"(v) : "memory");
-}
-__device__ __forceinline__ int ld_acquire(const int* p) {
-  int v;
-  asm volatile("ld.acquire.cta.shared::cta.b32 %0, [%1];" : "=r"(v) : "r"(smem_u32(p)) : "memory");
-  return v;
-}
 
 // Wait until a stage is free.  False after an abort: the consumers then release stages
 // without waiting for their copies, so nothing more may be issued.  Warp-uniform.
@@ -389,7 +381,7 @@ __device__ void q_produce_u(const QDecodeParams& p, const CUtensorMap* tmU, uint
       }
       uint64_t* full = &bar.u_full[us];
       if (lane == 0) {
-        st_release(&bar.useq[us], un);
+        bar.useq[us] = un;
         mbar_arrive_expect_tx(full, (per_agent ? __popc(need) : 1) * U_BYTES);
       }
       __syncwarp();
@@ -410,7 +402,7 @@ __device__ void q_produce_u(const QDecodeParams& p, const CUtensorMap* tmU, uint
 __device__ __forceinline__ void q_produce_meta(const QDecodeParams& p, const QBars& bar, const Range& range) {
   const int lane = threadIdx.x & 31;
   const bool paged = p.page_table != nullptr;
-  int stage = 0, n = 0, us = 0, un = 0;
+  int stage = 0, us = 0, un = 0;
   uint32_t phase = 0, uphase = 0;
   bool stop = p.stall != 0;
   Walk walk;
@@ -464,10 +456,9 @@ __device__ __forceinline__ void q_produce_meta(const QDecodeParams& p, const QBa
         m->us = has_u ? us : -1;
         m->un = un;
         m->uphase = uphase;
-        st_release(&m->n, n);
+        mbar_arrive(&bar.told[stage]);
       }
       __syncwarp();
-      ++n;
       if (++stage == p.stages) {
         stage = 0;
         phase ^= 1;
@@ -505,9 +496,10 @@ struct WarpRows {
   float w[NR];      // reference of O
   float l[NR];      // this lane's part of the row sum
   float o16[H16 ? D / 8 : 1][4];
-  float z16[H16 ? RK / 8 : 1][4];
   float o8[H8 ? D / 16 : 1][4];
-  float z8[H8 ? MZ : 1][4];
+  // Z^T of each eight rows: ranks 16 mz + g8 (+ 8), rows 8 x + 2 t4 (+ 1)
+  static constexpr int OCT = 2 * H16 + H8;
+  float z[OCT][MZ][4];
 };
 
 // Power of two that brings a row's largest |q| into [2^14, 2^15) (fp16 then holds
@@ -614,12 +606,12 @@ __device__ __forceinline__ uint32_t u_at(int k, int c) {
 __device__ __forceinline__ int slot_key(int s) { return s ^ ((s & 8) >> 1); }
 
 // Scores, softmax and values of one warp's keys (kw .. of the tile) of one tile; the
-// weights for the low-rank product are left in pz16 (rows as M) and pz8.  LAST: the
-// tile reaches past seq_len.
+// weights for the low-rank product are left in pz (of each 16 keys and eight rows, as
+// a B fragment) if want_z.  LAST: the tile reaches past seq_len.
 template <int FMT, int D, int RK, int H16, int H8, bool LAST>
 __device__ __forceinline__ void q_tile(WarpRows<D, RK, H16, H8>& st, int sl, uint32_t Ks, float ks_scale,
-                                       float vs_scale, int key0, int kw, const uint32_t* qs,
-                                       uint32_t (*pz16)[4], uint32_t (*pz8)[2]) {
+                                       float vs_scale, int key0, int kw, const uint32_t* qs, bool want_z,
+                                       uint32_t (*pz)[WarpRows<D, RK, H16, H8>::OCT][2]) {
   using WR = WarpRows<D, RK, H16, H8>;
   constexpr int KS = D / 16;
   constexpr int NB = kQWarpKeys / 16;  // blocks of 16 keys
@@ -630,13 +622,6 @@ __device__ __forceinline__ void q_tile(WarpRows<D, RK, H16, H8>& st, int sl, uin
 
   // ---- scores: S = Q K^T (16-row part), S^T = K Q^T (8-row part)
   float s16[H16 ? NB : 1][2][4], s8[H8 ? NB : 1][4];
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if constexpr (H16) s16[nb][0][e] = s16[nb][1][e] = 0.f;
-      if constexpr (H8) s8[nb][e] = 0.f;
-    }
   {
     // tiles are 1024-aligned and a row's chunk bits lie below its key bits, so
     // chunk 2 cc + c of a row is chunk c's address with bits 5 .. flipped by cc
@@ -677,11 +662,19 @@ __device__ __forceinline__ void q_tile(WarpRows<D, RK, H16, H8>& st, int sl, uin
           uint32_t a0, a2, b0, b2;
           codes_to_half2<FMT>(r[2 * h], a0, a2);
           codes_to_half2<FMT>(r[2 * h + 1], b0, b2);
-          if constexpr (H16) {
-            mma_f16_16816(s16[nb][0], q16[h][0], q16[h][1], q16[h][2], q16[h][3], a0, a2);
-            mma_f16_16816(s16[nb][1], q16[h][0], q16[h][1], q16[h][2], q16[h][3], b0, b2);
+          if (cc == 0 && h == 0) {
+            if constexpr (H16) {
+              mma_f16_16816_first(s16[nb][0], q16[h][0], q16[h][1], q16[h][2], q16[h][3], a0, a2);
+              mma_f16_16816_first(s16[nb][1], q16[h][0], q16[h][1], q16[h][2], q16[h][3], b0, b2);
+            }
+            if constexpr (H8) mma_f16_16816_first(s8[nb], a0, b0, a2, b2, q8[h][0], q8[h][1]);
+          } else {
+            if constexpr (H16) {
+              mma_f16_16816(s16[nb][0], q16[h][0], q16[h][1], q16[h][2], q16[h][3], a0, a2);
+              mma_f16_16816(s16[nb][1], q16[h][0], q16[h][1], q16[h][2], q16[h][3], b0, b2);
+            }
+            if constexpr (H8) mma_f16_16816(s8[nb], a0, b0, a2, b2, q8[h][0], q8[h][1]);
           }
-          if constexpr (H8) mma_f16_16816(s8[nb], a0, b0, a2, b2, q8[h][0], q8[h][1]);
         }
       }
     }
@@ -718,12 +711,12 @@ __device__ __forceinline__ void q_tile(WarpRows<D, RK, H16, H8>& st, int sl, uin
     if constexpr (H16) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        mx[i] = fmaxf(mx[i], fmaxf(fmaxf(s16[nb][0][2 * i], s16[nb][0][2 * i + 1]),
-                                   fmaxf(s16[nb][1][2 * i], s16[nb][1][2 * i + 1])));
+        mx[i] = max3(max3(mx[i], s16[nb][0][2 * i], s16[nb][0][2 * i + 1]), s16[nb][1][2 * i],
+                     s16[nb][1][2 * i + 1]);
     }
     if constexpr (H8) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) mx[R8 + i] = fmaxf(mx[R8 + i], fmaxf(s8[nb][i], s8[nb][2 + i]));
+      for (int i = 0; i < 2; ++i) mx[R8 + i] = max3(mx[R8 + i], s8[nb][i], s8[nb][2 + i]);
     }
   }
   // The scale is >= 0 and rounding monotonic: the scaled maximum is the maximum of
@@ -758,9 +751,13 @@ __device__ __forceinline__ void q_tile(WarpRows<D, RK, H16, H8>& st, int sl, uin
 #pragma unroll
         for (int e = 0; e < 4; ++e) st.o16[x][e] *= be[e >> 1];
 #pragma unroll
-      for (int x = 0; x < RK / 8; ++x)
+      for (int x = 0; x < 2; ++x) {  // rows 2 t4, 2 t4 + 1 belong to the lanes with g8 = 2 t4, 2 t4 + 1
+        const float a0 = __shfl_sync(0xFFFFFFFFu, al[x], 8 * t4), a1 = __shfl_sync(0xFFFFFFFFu, al[x], 8 * t4 + 4);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) st.z16[x][e] *= al[e >> 1];
+        for (int mz = 0; mz < WR::MZ; ++mz)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) st.z[x][mz][e] *= e & 1 ? a1 : a0;
+      }
     }
     if constexpr (H8) {
 #pragma unroll
@@ -770,7 +767,7 @@ __device__ __forceinline__ void q_tile(WarpRows<D, RK, H16, H8>& st, int sl, uin
 #pragma unroll
       for (int x = 0; x < WR::MZ; ++x)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) st.z8[x][e] *= al[R8 + (e & 1)];
+        for (int e = 0; e < 4; ++e) st.z[2 * H16][x][e] *= al[R8 + (e & 1)];
     }
   }
   float mu[NR], f[NR];
@@ -787,11 +784,11 @@ __device__ __forceinline__ void q_tile(WarpRows<D, RK, H16, H8>& st, int sl, uin
 #pragma unroll
       for (int x = 0; x < 2; ++x)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {  // A fragment: rows g8, g8 + 8 of slots 2 t4 + 8 x (+ 1)
+        for (int i = 0; i < 2; ++i) {  // A fragment: rows g8 + 8 i of slots 2 t4 + 8 x (+ 1)
           const float p0 = fast_exp2(fmaf(s16[nb][x][2 * i], sc[i], -mu[i]));
           const float p1 = fast_exp2(fmaf(s16[nb][x][2 * i + 1], sc[i], -mu[i]));
           st.l[i] += p0 + p1;
-          pz16[nb][2 * x + i] = pack_bf16x2(p0, p1);
+          if (want_z) pz[nb][i][x] = pack_bf16x2(p0, p1);  // of rows 8 i ..: the same layout
           pv16[nb][2 * x + i] = pack_f16x2(p0 * f[i], p1 * f[i]);
         }
     }
@@ -802,7 +799,7 @@ __device__ __forceinline__ void q_tile(WarpRows<D, RK, H16, H8>& st, int sl, uin
         const float p1 = fast_exp2(fmaf(s8[nb][2 * x + 1], sc[R8 + 1], -mu[R8 + 1]));
         st.l[R8] += p0;
         st.l[R8 + 1] += p1;
-        pz8[nb][x] = movmatrix_t(pack_bf16x2(p0, p1));
+        if (want_z) pz[nb][2 * H16][x] = movmatrix_t(pack_bf16x2(p0, p1));
         pv8[nb][x] = movmatrix_t(pack_f16x2(p0 * f[R8], p1 * f[R8 + 1]));
       }
     }
@@ -840,14 +837,15 @@ __device__ __forceinline__ void q_tile(WarpRows<D, RK, H16, H8>& st, int sl, uin
 
 }
 
-// Low-rank values of the same keys: Z += P U_i over each agent's own rows.  `agents`
-// has a bit for every agent of this warp's rows whose U tile counts here; U rows
-// before a_i or at or past seq_len are selected out (`clean`: there are none).
+// Low-rank values of the same keys: Z^T += U_i^T P^T over each agent's own rows, eight
+// rows at a time.  `agents` has a bit for every agent of this warp's rows whose U tile
+// counts here; U rows before a_i or at or past seq_len are selected out (`clean`: there
+// are none).  w_lo: the warp's first row, counted from the first agent's first.
 template <int D, int RK, int H16, int H8>
-__device__ __forceinline__ void q_low_rank(WarpRows<D, RK, H16, H8>& st, const uint32_t (*pz16)[4],
-                                           const uint32_t (*pz8)[2], uint32_t Us, int slot_bytes, unsigned agents,
-                                           bool one_pass, const int* my_ag, bool clean, const int* a_sm, int key0,
-                                           int kw, int sl) {
+__device__ __forceinline__ void q_low_rank(WarpRows<D, RK, H16, H8>& st,
+                                           const uint32_t (*pz)[WarpRows<D, RK, H16, H8>::OCT][2], uint32_t Us,
+                                           int slot_bytes, unsigned agents, bool one_pass, const int* my_ag, int G,
+                                           int w_lo, bool clean, const int* a_sm, int key0, int kw, int sl) {
   using WR = WarpRows<D, RK, H16, H8>;
   constexpr int NB = kQWarpKeys / 16;
   const int lane = threadIdx.x & 31, t4 = lane & 3, j = lane >> 3;
@@ -856,43 +854,43 @@ __device__ __forceinline__ void q_low_rank(WarpRows<D, RK, H16, H8>& st, const u
     const int ag = __ffs(agents) - 1;
     agents &= agents - 1;
     const uint32_t ub = at + ag * slot_bytes;
-    bool use[2 * H16 + H8];
+    uint32_t u[NB][WR::MZ][4];  // ranks 16 mz + g8: slots 0-7, 8-15; ranks + 8 likewise
 #pragma unroll
-    for (int i = 0; i < 2 * H16 + H8; ++i) use[i] = one_pass || my_ag[i] == ag;
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      uint32_t a16[4], b8[2];
-      if constexpr (H16) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) a16[i] = use[i & 1] ? pz16[nb][i] : 0u;
-      }
-      if constexpr (H8) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) b8[i] = use[2 * H16] ? pz8[nb][i] : 0u;
-      }
-      uint32_t um_lo = 0xFFFFFFFFu, um_hi = 0xFFFFFFFFu;
-      if (!clean) {
-        const int a_i = one_pass ? 0 : a_sm[ag];
-        const int x = key0 + kw + 16 * nb + 2 * t4, y = key0 + kw + 16 * nb + 8 + ((2 * t4) ^ 4);
-        um_lo = (x >= a_i && x < sl ? 0xFFFFu : 0u) | (x + 1 >= a_i && x + 1 < sl ? 0xFFFF0000u : 0u);
-        um_hi = (y >= a_i && y < sl ? 0xFFFFu : 0u) | (y + 1 >= a_i && y + 1 < sl ? 0xFFFF0000u : 0u);
-      }
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int mz = 0; mz < WR::MZ; ++mz) {
-        uint32_t r0, r1, r2 = 0, r3 = 0;  // ranks 16 mz + g8: slots 0-7, 8-15; ranks + 8 likewise
-        if constexpr (RK == 8) ldsm_x2_t(r0, r1, ub + nb * 256);
-        else ldsm_x4_t(r0, r1, r2, r3, (ub ^ (mz << 5)) + nb * 32 * RK);
-        if (!clean) {
-          r0 &= um_lo;
-          r1 &= um_hi;
-          r2 &= um_lo;
-          r3 &= um_hi;
+        uint32_t* r = u[nb][mz];
+        r[2] = r[3] = 0;
+        if constexpr (RK == 8) ldsm_x2_t(r[0], r[1], ub + nb * 256);
+        else ldsm_x4_t(r[0], r[1], r[2], r[3], (ub ^ (mz << 5)) + nb * 32 * RK);
+      }
+    if (!clean) {
+      const int a_i = one_pass ? 0 : a_sm[ag];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const int x = key0 + kw + 16 * nb + 2 * t4, y = key0 + kw + 16 * nb + 8 + ((2 * t4) ^ 4);
+        const uint32_t lo = (x >= a_i && x < sl ? 0xFFFFu : 0u) | (x + 1 >= a_i && x + 1 < sl ? 0xFFFF0000u : 0u);
+        const uint32_t hi = (y >= a_i && y < sl ? 0xFFFFu : 0u) | (y + 1 >= a_i && y + 1 < sl ? 0xFFFF0000u : 0u);
+#pragma unroll
+        for (int mz = 0; mz < WR::MZ; ++mz) {
+          u[nb][mz][0] &= lo;
+          u[nb][mz][1] &= hi;
+          u[nb][mz][2] &= lo;
+          u[nb][mz][3] &= hi;
         }
-        if constexpr (H16) {
-          mma_bf16_16816(st.z16[RK == 8 ? 0 : 2 * mz], a16[0], a16[1], a16[2], a16[3], r0, r1);
-          if constexpr (RK > 8) mma_bf16_16816(st.z16[2 * mz + 1], a16[0], a16[1], a16[2], a16[3], r2, r3);
-        }
-        if constexpr (H8) mma_bf16_16816(st.z8[mz], r0, r2, r1, r3, b8[0], b8[1]);
+      }
+    }
+    const int r_lo = one_pass ? 0 : ag * G - w_lo, r_hi = one_pass ? WR::RPW : r_lo + G;  // the agent's rows
+#pragma unroll
+    for (int x = 0; x < WR::OCT; ++x) {
+      if (r_lo >= 8 * x + 8 || r_hi <= 8 * x) continue;  // warp-uniform
+      const bool use = one_pass || my_ag[x] == ag;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const uint32_t b0 = use ? pz[nb][x][0] : 0u, b1 = use ? pz[nb][x][1] : 0u;
+#pragma unroll
+        for (int mz = 0; mz < WR::MZ; ++mz)
+          mma_bf16_16816(st.z[x][mz], u[nb][mz][0], u[nb][mz][2], u[nb][mz][1], u[nb][mz][3], b0, b1);
       }
     }
   }
@@ -1002,21 +1000,17 @@ __device__ __forceinline__ void merge_warps(WarpRows<D, RK, H16, H8>& st, float*
     }
     reduce(mO + c0, D, CW);
   }
-  if constexpr (H16) {
 #pragma unroll
-    for (int x = 0; x < RK / 8; ++x)
+  for (int x = 0; x < WR::OCT; ++x) {
+    // fz of rows 2 t4, 2 t4 + 1 of these eight
+    const float f0 = x < 2 * H16 ? __shfl_sync(0xFFFFFFFFu, fz[x], 8 * t4) : fz[NR - 2];
+    const float f1 = x < 2 * H16 ? __shfl_sync(0xFFFFFFFFu, fz[x], 8 * t4 + 4) : fz[NR - 1];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        *reinterpret_cast<float2*>(mine + row[i] * CW + 8 * x + 2 * t4) =
-            make_float2(st.z16[x][2 * i] * fz[i], st.z16[x][2 * i + 1] * fz[i]);
-  }
-  if constexpr (H8) {
-#pragma unroll
-    for (int x = 0; x < WR::MZ; ++x)
+    for (int mz = 0; mz < WR::MZ; ++mz)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (16 * x + 8 * (e >> 1) < RK)
-          mine[row[R8 + (e & 1)] * CW + 16 * x + 8 * (e >> 1) + g8] = st.z8[x][e] * fz[R8 + (e & 1)];
+        if (16 * mz + 8 * (e >> 1) < RK)
+          mine[(8 * x + 2 * t4 + (e & 1)) * CW + 16 * mz + 8 * (e >> 1) + g8] = st.z[x][mz][e] * (e & 1 ? f1 : f0);
   }
   reduce(mZ, RK, RK);
 }
@@ -1173,19 +1167,18 @@ __device__ __forceinline__ void finish_item(const QDecodeParams& p, const Range&
   }
 }
 
-// Wait until a stage belongs to tile number n, then for its bytes.
-__device__ __forceinline__ void q_wait(const QDecodeParams& p, const int* seq, int n, uint64_t* full, uint32_t phase,
-                                       volatile int* abort_flag) {
+// Wait until a U stage holds U tile number un, then for its bytes.
+__device__ __forceinline__ void q_wait_u(const QDecodeParams& p, const QBars& bar, int us, int un, uint32_t phase) {
   uint32_t spins = 0;
-  while (ld_acquire(seq) != n) {
-    if (*abort_flag) break;
+  while (bar.useq[us] != un) {
+    if (*bar.abort_flag) break;
     if (++spins >= p.spin_cap) {
-      *abort_flag = 1;
+      *bar.abort_flag = 1;
       atomicOr(p.flags, LRKV_DEVFLAG_TIMEOUT);
       break;
     }
   }
-  mbar_wait_bounded(full, phase, abort_flag, p.flags, p.spin_cap, true);
+  mbar_wait_bounded(&bar.u_full[us], phase, bar.abort_flag, p.flags, p.spin_cap, true);
 }
 
 template <int FMT, int D, int RK, int H16, int H8, int NRB>
@@ -1234,39 +1227,40 @@ __device__ void q_consumers(const QDecodeParams& p, uint8_t* smem, const QDecode
     if constexpr (H16) {
 #pragma unroll
       for (int x = 0; x < D / 8; ++x) st.o16[x][0] = st.o16[x][1] = st.o16[x][2] = st.o16[x][3] = 0.f;
-#pragma unroll
-      for (int x = 0; x < RK / 8; ++x) st.z16[x][0] = st.z16[x][1] = st.z16[x][2] = st.z16[x][3] = 0.f;
     }
     if constexpr (H8) {
 #pragma unroll
       for (int x = 0; x < D / 16; ++x) st.o8[x][0] = st.o8[x][1] = st.o8[x][2] = st.o8[x][3] = 0.f;
-#pragma unroll
-      for (int x = 0; x < WR::MZ; ++x) st.z8[x][0] = st.z8[x][1] = st.z8[x][2] = st.z8[x][3] = 0.f;
     }
+#pragma unroll
+    for (int x = 0; x < WR::OCT; ++x)
+#pragma unroll
+      for (int mz = 0; mz < WR::MZ; ++mz) st.z[x][mz][0] = st.z[x][mz][1] = st.z[x][mz][2] = st.z[x][mz][3] = 0.f;
 
     before += sg.sl > 0 ? sg.hi - sg.lo : 0;  // an empty session has no tiles
     while (n < before) {
+      mbar_wait_bounded(&bar.told[stage], phase, bar.abort_flag, p.flags, p.spin_cap, true);
       const Meta* meta = bar.meta + stage;
-      q_wait(p, &meta->n, n, &bar.full[stage], phase, bar.abort_flag);
       const float2 scales = *reinterpret_cast<const float2*>(meta);
       const int key0 = meta->key0, us = meta->us;
+      mbar_wait_bounded(&bar.full[stage], phase, bar.abort_flag, p.flags, p.spin_cap, true);
       const bool last = key0 + kQBlock > sg.sl;
-      uint32_t pz16[H16 ? NB : 1][4], pz8[H8 ? NB : 1][2];
+      uint32_t pz[NB][WR::OCT][2];
       const uint32_t Ks = ring + stage * lay.tile_bytes;
       if (key0 >= 0) {
-        if (last) q_tile<FMT, D, RK, H16, H8, true>(st, sg.sl, Ks, scales.x, scales.y, key0, kw, qs, pz16, pz8);
-        else q_tile<FMT, D, RK, H16, H8, false>(st, sg.sl, Ks, scales.x, scales.y, key0, kw, qs, pz16, pz8);
+        if (last) q_tile<FMT, D, RK, H16, H8, true>(st, sg.sl, Ks, scales.x, scales.y, key0, kw, qs, us >= 0, pz);
+        else q_tile<FMT, D, RK, H16, H8, false>(st, sg.sl, Ks, scales.x, scales.y, key0, kw, qs, us >= 0, pz);
       }
       if (us >= 0) {
-        q_wait(p, &bar.useq[us], meta->un, &bar.u_full[us], meta->uphase, bar.abort_flag);
+        q_wait_u(p, bar, us, meta->un, meta->uphase);
         if (key0 >= 0) {
           const bool one_pass = p.mode == LRKV_BASE_LR_SHARED && !last && a_max <= key0;
           const unsigned mine = __ballot_sync(0xFFFFFFFFu, lane >= ag_lo && lane <= ag_hi && key0 + kQBlock > lane_a);
           const bool clean = !last && !__any_sync(0xFFFFFFFFu, (mine >> lane & 1) && lane_a > key0);
-          q_low_rank<D, RK, H16, H8>(st, pz16, pz8, ring + lay.u_off + us * lay.u_bytes,
+          q_low_rank<D, RK, H16, H8>(st, pz, ring + lay.u_off + us * lay.u_bytes,
                                      p.mode == LRKV_BASE_SHARED ? kQBlock * RK * 2 : 0,
-                                     one_pass ? mine & (0u - mine) : mine, one_pass, my_ag, clean, a_sm, key0, kw,
-                                     sg.sl);
+                                     one_pass ? mine & (0u - mine) : mine, one_pass, my_ag, p.G,
+                                     w_lo - sg.i_lo * p.G, clean, a_sm, key0, kw, sg.sl);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.u_empty[us]);
@@ -1303,10 +1297,11 @@ __global__ void __launch_bounds__(kQBlockThreads, 1)
   QBars bar;
   bar.full = reinterpret_cast<uint64_t*>(smem + lay.bar_off);
   bar.empty = bar.full + p.stages;
-  bar.u_full = bar.empty + p.stages;
+  bar.told = bar.empty + p.stages;
+  bar.u_full = bar.told + p.stages;
   bar.u_empty = bar.u_full + p.u_stages;
   bar.meta = reinterpret_cast<Meta*>(smem + lay.meta_off);
-  bar.useq = reinterpret_cast<int*>(smem + lay.useq_off);
+  bar.useq = reinterpret_cast<volatile int*>(smem + lay.useq_off);
   Range* range = reinterpret_cast<Range*>(smem + lay.misc_off);
   bar.abort_flag = reinterpret_cast<volatile int*>(range + 1);
   int* bcast = const_cast<int*>(bar.abort_flag) + 1;
@@ -1315,8 +1310,8 @@ __global__ void __launch_bounds__(kQBlockThreads, 1)
     constexpr int READERS = kQBlock / kQWarpKeys * NRB;  // warps that read a tile
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&bar.full[s], 1);
+      mbar_init(&bar.told[s], 1);
       mbar_init(&bar.empty[s], READERS);
-      bar.meta[s].n = -1;
     }
     for (int s = 0; s < p.u_stages; ++s) {
       mbar_init(&bar.u_full[s], 1);

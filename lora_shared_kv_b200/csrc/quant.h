@@ -90,6 +90,8 @@ __host__ __device__ constexpr QShape q_shape(int rows) {
   return rows <= 8 ? QShape{0, 1, 1} : rows <= 16 ? QShape{1, 0, 1} : rows <= 24 ? QShape{1, 1, 1} : QShape{1, 0, 2};
 }
 
+__host__ __device__ constexpr int q_groups(int nrb) { return kQWarps / (kQBlock / kQWarpKeys) / nrb; }
+
 // Columns of O that the warps exchange per pass when their rows are merged.
 constexpr int kQMergeCols = 32;
 
@@ -112,7 +114,7 @@ __host__ __device__ inline QDecodeSmem q_smem_plan(int D, int RK, int rows_block
   s.meta_off = s.q_off + (rows_block == 24 ? 24 * D * 2 : 0);            // what the producer tells of each stage
   s.a_off = s.meta_off + stages * 32;                                    // offsets of the item's agents
   s.bar_off = round_up(s.a_off + kMaxAgents * 4, 16);
-  s.useq_off = s.bar_off + 2 * (stages + u_stages) * 8;                  // tile number of each U stage
+  s.useq_off = s.bar_off + (3 * stages + 2 * u_stages) * 8;                 // tile number of each U stage
   s.misc_off = round_up(s.useq_off + u_stages * 4, 16);                  // the CTA's range, abort word, broadcast word
   s.total = s.misc_off + 96;
   return s;

@@ -129,16 +129,17 @@ lrkv_status plan_decode_quant(const lrkv_problem* p, int max_seq_len, const Devi
   const int rows_block = 16 * sh.h16 + 8 * sh.h8;
   pl->RP = rows_block * sh.nrb;
   // Up to four U stages within 80 KB (one per tile being worked on), then as many
-  // K/V stages as fit, up to 16.
+  // K/V stages as fit, up to 16, in multiples of the consumer groups.
   const int optin = dev.smem_optin > 0 ? dev.smem_optin : 232448;
   const int u_bytes = pl->n_u_slots * LRKV_QUANT_BLOCK * p->rank * 2;
   pl->u_stages = u_bytes > 81920 / 2 ? 1 : u_bytes * 4 > 81920 ? 81920 / u_bytes : 4;
   auto smem_of = [&](int stages) {
     return lrkv::q_smem_plan(p->head_dim, p->rank, rows_block, sh.nrb, pl->n_u_slots, stages, pl->u_stages).total + 1024;
   };
+  const int groups = lrkv::q_groups(sh.nrb);
   int stages = 16;
-  while (stages >= 2 && smem_of(stages) > optin) --stages;
-  if (stages < 2) return fail(LRKV_ERR_UNSUPPORTED, "decode tiles do not fit in shared memory");
+  while (stages >= groups && smem_of(stages) > optin) stages -= groups;
+  if (stages < groups) return fail(LRKV_ERR_UNSUPPORTED, "decode tiles do not fit in shared memory");
   pl->stages = stages;
   pl->smem = smem_of(stages);
   pl->tickets_off = lrkv::kWsHeaderBytes;
