@@ -521,8 +521,9 @@ __device__ __forceinline__ const __nv_bfloat16* q_row(const QDecodeParams& p, co
 }
 
 // The row block's queries as fp16 fragments.  A lane's four dims of a 16-dim step
-// are 4 t4 .. + 3 (the bytes that ldmatrix gives it of K).
-template <int D, int RK, int H16, int H8>
+// are 4 t4 .. + 3 (the bytes that ldmatrix gives it of K), in the order of the codes'
+// fp16 pairs.
+template <int FMT, int D, int RK, int H16, int H8>
 __device__ __forceinline__ void load_queries(const QDecodeParams& p, const Seg& sg, int rbase,
                                              WarpRows<D, RK, H16, H8>& st, uint32_t* qs) {
   using WR = WarpRows<D, RK, H16, H8>;
@@ -554,8 +555,10 @@ __device__ __forceinline__ void load_queries(const QDecodeParams& p, const Seg& 
     uint32_t f16[4] = {}, f8[2] = {};
 #pragma unroll
     for (int i = 0; i < PARTS; ++i) {
-      const uint32_t lo = pack_f16x2(bf_lo(raw[i][ks].x) * f[i], bf_hi(raw[i][ks].x) * f[i]);
-      const uint32_t hi = pack_f16x2(bf_lo(raw[i][ks].y) * f[i], bf_hi(raw[i][ks].y) * f[i]);
+      const float d[4] = {bf_lo(raw[i][ks].x) * f[i], bf_hi(raw[i][ks].x) * f[i], bf_lo(raw[i][ks].y) * f[i],
+                          bf_hi(raw[i][ks].y) * f[i]};
+      const uint32_t lo = pack_f16x2(d[code_byte<FMT>(0)], d[code_byte<FMT>(1)]);
+      const uint32_t hi = pack_f16x2(d[code_byte<FMT>(2)], d[code_byte<FMT>(3)]);
       if (H16 && i < 2) {
         f16[i] = lo;
         f16[i + 2] = hi;
@@ -607,8 +610,11 @@ __device__ __forceinline__ int slot_key(int s) { return s ^ ((s & 8) >> 1); }
 
 // Scores, softmax and values of one warp's keys (kw .. of the tile) of one tile; the
 // weights for the low-rank product are left in pz (of each 16 keys and eight rows, as
-// a B fragment) if want_z.  LAST: the tile reaches past seq_len.
-template <int FMT, int D, int RK, int H16, int H8, bool LAST>
+// a B fragment) if want_z.
+// A tile that reaches past seq_len: its value codes past it are zeroed in shared memory
+// first, and its scores past it selected out.  (One path for every tile: two instances
+// of this code cost a copy of every accumulator where they meet.)
+template <int FMT, int D, int RK, int H16, int H8>
 __device__ __forceinline__ void q_tile(WarpRows<D, RK, H16, H8>& st, int sl, uint32_t Ks, float ks_scale,
                                        float vs_scale, int key0, int kw, const uint32_t* qs, bool want_z,
                                        uint32_t (*pz)[WarpRows<D, RK, H16, H8>::OCT][2]) {
@@ -619,6 +625,13 @@ __device__ __forceinline__ void q_tile(WarpRows<D, RK, H16, H8>& st, int sl, uin
   constexpr int R8 = WR::R8;
   const int lane = threadIdx.x & 31, g8 = lane >> 2, t4 = lane & 3;
   const uint32_t Vs = Ks + kQBlock * D;
+  const bool last = key0 + kQBlock > sl;
+  if (last) {
+    for (int k = max(sl - key0, kw); k < kw + kQWarpKeys; ++k)
+      if (lane < D / 16) st_shared_zero16(Vs + k * D + lane * 16);
+    fence_proxy_async_smem();  // ahead of the copy that fills this stage next
+    __syncwarp();
+  }
 
   // ---- scores: S = Q K^T (16-row part), S^T = K Q^T (8-row part)
   float s16[H16 ? NB : 1][2][4], s8[H8 ? NB : 1][4];
@@ -683,7 +696,7 @@ __device__ __forceinline__ void q_tile(WarpRows<D, RK, H16, H8>& st, int sl, uin
   // ---- softmax
   const int k_lo = key0 + kw + 2 * t4;                 // keys of slots 2 t4 (+ 1)
   const int k_hi = key0 + kw + 8 + ((2 * t4) ^ 4);     // keys of slots 2 t4 + 8 (+ 9)
-  if constexpr (LAST) {  // keys at or past seq_len are selected out
+  if (last) {  // keys at or past seq_len are selected out
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       if constexpr (H16) {
@@ -807,14 +820,15 @@ __device__ __forceinline__ void q_tile(WarpRows<D, RK, H16, H8>& st, int sl, uin
 
   // ---- values: O += P V, O^T += V^T P^T
   {
-    const int e = lane & 15;  // row of a 16 x 16 block: slots 2t, 2t + 1, 2t + 8, 2t + 9 for rows 4t ..
-    const uint32_t at = Vs + tile_at<D>(kw + slot_key(2 * (e >> 2) + (e & 1) + 8 * ((e >> 1) & 1)), lane >> 4);
+    // row 4 t + e of a 16 x 16 block becomes byte e of lane t: slots 2 t, 2 t + 1 (the
+    // fp16 pair lo) and 2 t + 8, 2 t + 9 (hi)
+    const int e = lane & 15;
+    int i = 0;  // which element of the pairs byte e & 3 is
+#pragma unroll
+    for (int x = 0; x < 4; ++x) i = code_byte<FMT>(x) == (e & 3) ? x : i;
+    const uint32_t at = Vs + tile_at<D>(kw + slot_key(2 * (e >> 2) + (i & 1) + 8 * (i >> 1)), lane >> 4);
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      uint32_t vm = 0xFFFFFFFFu;  // a lane's four codes belong to four keys
-      if constexpr (LAST)
-        vm = (k_lo + 16 * nb < sl ? 0xFFu : 0u) | (k_lo + 16 * nb + 1 < sl ? 0xFF00u : 0u) |
-             (k_hi + 16 * nb < sl ? 0xFF0000u : 0u) | (k_hi + 16 * nb + 1 < sl ? 0xFF000000u : 0u);
 #pragma unroll
       for (int cc = 0; cc < KS / 2; ++cc) {
         uint32_t r[4];  // dims 32 cc + 8 x + g8
@@ -822,8 +836,8 @@ __device__ __forceinline__ void q_tile(WarpRows<D, RK, H16, H8>& st, int sl, uin
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t a0, a1, b0, b1;
-          codes_to_half2<FMT>(LAST ? r[2 * h] & vm : r[2 * h], a0, a1);
-          codes_to_half2<FMT>(LAST ? r[2 * h + 1] & vm : r[2 * h + 1], b0, b1);
+          codes_to_half2<FMT>(r[2 * h], a0, a1);
+          codes_to_half2<FMT>(r[2 * h + 1], b0, b1);
           if constexpr (H16) {
             float* o = st.o16[4 * cc + 2 * h];
             mma_f16_16816(o, pv16[nb][0], pv16[nb][1], pv16[nb][2], pv16[nb][3], a0, a1);
@@ -1207,7 +1221,7 @@ __device__ void q_consumers(const QDecodeParams& p, uint8_t* smem, const QDecode
   WR st;
   while (walk.next(p, sg)) {
     if (tid < sg.n_ag) a_sm[tid] = load_offset(p, sg.s, sg.i_lo + tid, true);
-    load_queries<D, RK, H16, H8>(p, sg, rb * RPW, st, qs);
+    load_queries<FMT, D, RK, H16, H8>(p, sg, rb * RPW, st, qs);
     q_sync();
     // this lane's agent's offset (lane j: agent j), and the item's largest
     const int lane_a = lane < sg.n_ag ? a_sm[lane] : 0x7fffffff;
@@ -1248,8 +1262,7 @@ __device__ void q_consumers(const QDecodeParams& p, uint8_t* smem, const QDecode
       uint32_t pz[NB][WR::OCT][2];
       const uint32_t Ks = ring + stage * lay.tile_bytes;
       if (key0 >= 0) {
-        if (last) q_tile<FMT, D, RK, H16, H8, true>(st, sg.sl, Ks, scales.x, scales.y, key0, kw, qs, us >= 0, pz);
-        else q_tile<FMT, D, RK, H16, H8, false>(st, sg.sl, Ks, scales.x, scales.y, key0, kw, qs, us >= 0, pz);
+        q_tile<FMT, D, RK, H16, H8>(st, sg.sl, Ks, scales.x, scales.y, key0, kw, qs, us >= 0, pz);
       }
       if (us >= 0) {
         q_wait_u(p, bar, us, meta->un, meta->uphase);

@@ -153,10 +153,10 @@ __device__ __forceinline__ void decode4(uint32_t w, float* f) {
   codes_to_half2<FMT>(w, lo, hi);
   const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
   const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-  f[0] = a.x;
-  f[1] = a.y;
-  f[2] = b.x;
-  f[3] = b.y;
+  f[code_byte<FMT>(0)] = a.x;
+  f[code_byte<FMT>(1)] = a.y;
+  f[code_byte<FMT>(2)] = b.x;
+  f[code_byte<FMT>(3)] = b.y;
 }
 
 template <int FMT, int D>

@@ -8,9 +8,12 @@
 namespace lrkv {
 
 // Four codes (bytes 0 .. 3 of w) as two fp16 pairs, exact.
-//   e4m3: one conversion per pair.
-//   int8: fp16 0x6400 | u is 1024 + u, so with u = code + 128 the subtraction of
-//         1152 leaves the code.
+//   e4m3: lo = bytes 0, 1 and hi = bytes 2, 3; one conversion per pair.
+//   int8: lo = bytes 0, 2 and hi = bytes 1, 3: fp16 0x6400 | u is 1024 + u, so with
+//         u = code + 128 the subtraction of 1152 leaves the code.  The shift that
+//         brings bytes 1, 3 down is a multiplication's high word: the integer
+//         pipe, which the masks (and the rest of the tile's work) load, is the
+//         busier one.
 template <int FMT>
 __device__ __forceinline__ void codes_to_half2(uint32_t w, uint32_t& lo, uint32_t& hi) {
   if constexpr (FMT == LRKV_Q_E4M3) {
@@ -21,12 +24,16 @@ __device__ __forceinline__ void codes_to_half2(uint32_t w, uint32_t& lo, uint32_
         : "=r"(lo), "=r"(hi)
         : "r"(w));
   } else {
-    const uint32_t u = w ^ 0x80808080u;
-    lo = __byte_perm(u, 0x64646464u, 0x4140);
-    hi = __byte_perm(u, 0x64646464u, 0x4342);
+    lo = (w & 0x00FF00FFu) ^ 0x64806480u;
+    hi = (__umulhi(w, 1u << 24) & 0x00FF00FFu) ^ 0x64806480u;
     asm("sub.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(0x64806480u));
     asm("sub.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(0x64806480u));
   }
+}
+// Which byte of w element `i` (0, 1: of lo; 2, 3: of hi) comes from.
+template <int FMT>
+__host__ __device__ constexpr int code_byte(int i) {
+  return FMT == LRKV_Q_E4M3 ? i : (i & 1) * 2 + (i >> 1);
 }
 
 // 16 bytes that are read once.
@@ -36,6 +43,10 @@ __device__ __forceinline__ uint4 ld_stream(const void* p) {
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
+}
+
+__device__ __forceinline__ void st_shared_zero16(uint32_t addr) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0u) : "memory");
 }
 
 // Two 16 x 16 blocks of bytes, transposed: lane l gets rows 4 (l % 4) .. + 3 of
