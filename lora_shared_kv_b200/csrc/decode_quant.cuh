@@ -50,25 +50,34 @@ namespace {
 constexpr float kNegInf = -INFINITY;
 constexpr int kMergeBatch = 4;  // partial records whose loads are in flight together
 
-// The CTA's share of the work, found by warp 0.
+// The CTA's share of the work, found by warp 0.  Tiles of a launch are counted in 32
+// bits (checked on the host).
 struct Range {
-  long long W, t_begin, t_end;  // tiles of the launch; this CTA's
-  long long base;               // first tile of session s
-  int s;                        // session of t_begin
-  int ctas;                     // CTAs that take part
-  int whole;                    // whole items, one per CTA
-  int pad;
+  int W, ctas;          // tiles of the launch; CTAs that take part
+  int t_begin, t_end;   // this CTA's tiles
+  int s, base, sl;      // session of t_begin, its first tile, its length
+  int whole;            // whole items, one per CTA
 };
 
-// What the meta warp tells of the tile in a stage.
-struct __align__(16) Meta {
+// First tile of CTA c when W tiles are split evenly: floor(c W / C), in 32 bits.
+__device__ __forceinline__ int range_begin(int c, int W, int C) {
+  const int q = W / C;
+  return c * q + c * (W - q * C) / C;
+}
+
+// What the planner tells of a tile.
+struct __align__(16) Entry {
+  int key0;      // the tile's first key; kBadTile: not copied; kNoTile: the CTA's tiles end here
+  int c3;        // page (paged) or session: the K/V copies' outermost coordinate
+  int head;      // KV head | first agent << 16
+  int session;
   float ks, vs;  // the block's scales
-  int key0;      // the tile's first key; -1: not copied (a bad page id)
-  int us;        // U stage, -1: the tile needs none
+  int u;         // agents whose U tile is copied (16 bits) | U stage << 16 | its phase << 24; 0: none
   int un;        // number of the U tile among the CTA's
-  int uphase;
-  int pad[2];
 };
+constexpr int kBadTile = -1, kNoTile = -2;
+constexpr int kPlan = 32;   // tiles of a planned chunk
+constexpr int kPlans = 4;   // chunks of the table
 
 __device__ __forceinline__ int clamp_len(const QDecodeParams& p, int sl) {
   sl = sl < 0 ? 0 : sl;
@@ -83,66 +92,58 @@ __device__ __forceinline__ int tiles_of(int sl) { return sl > 0 ? (sl + kQBlock 
 __device__ __forceinline__ void find_range(const QDecodeParams& p, Range* out) {
   const int lane = threadIdx.x & 31;
   const int HR = p.Hkv * p.n_rg;
-  long long total = 0;
-  int nt_max = 0;
+  int total = 0, nt_max = 0, sl = 0;
   bool bad = false;
   for (int s0 = 0; s0 < p.S; s0 += 32) {
     const int s = s0 + lane;
-    int nt = 0;
     if (s < p.S) {
-      const int sl = __ldg(p.seq_lens + s);
-      bad |= sl != clamp_len(p, sl);
-      nt = tiles_of(clamp_len(p, sl));
+      const int given = __ldg(p.seq_lens + s);
+      sl = clamp_len(p, given);
+      bad |= sl != given;
+      total += tiles_of(sl);
+      nt_max = max(nt_max, tiles_of(sl));
     }
-    total += nt;
-    nt_max = max(nt_max, nt);
   }
   if (blockIdx.x == 0 && __any_sync(0xFFFFFFFFu, bad) && lane == 0) atomicOr(p.flags, LRKV_DEVFLAG_SEQLEN);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+  total = __reduce_add_sync(0xFFFFFFFFu, total);
   nt_max = __reduce_max_sync(0xFFFFFFFFu, nt_max);
-  const long long W = total * HR;
-  const long long items = (long long)p.S * HR;
-  const int C = (int)(W < (long long)gridDim.x ? W : (long long)gridDim.x);
-  const bool whole = q_whole_items(items, C, nt_max, W, p.whole_slack);
-  const int c = blockIdx.x;
-  const int ctas = whole ? (int)items : C;
+  const int W = total * HR, items = p.S * HR, c = blockIdx.x;
+  const int C = W < (int)gridDim.x ? W : (int)gridDim.x;
   Range r = {};
   r.W = W;
-  r.ctas = ctas;
-  r.whole = whole;
-  if (c < ctas) {
-    long long t0 = whole ? 0 : c * W / ctas;
-    r.t_end = whole ? 0 : (c + 1) * W / ctas;
+  r.whole = q_whole_items(items, C, nt_max, W, p.whole_slack);
+  r.ctas = r.whole ? items : C;
+  if (c < r.ctas) {
+    r.t_begin = r.whole ? 0 : range_begin(c, W, C);
+    r.t_end = r.whole ? 0 : range_begin(c + 1, W, C);
     const int s_whole = c / HR;
     // the session that holds the first tile (or item), and its first tile
-    long long base = 0;
-    for (int s0 = 0; s0 < p.S; s0 += 32) {
+    for (int s0 = 0, base = 0; s0 < p.S; s0 += 32) {
       const int s = s0 + lane;
-      const int nt = s < p.S ? tiles_of(session_len(p, s)) : 0;
-      int incl = nt;  // at most 32 sessions of 2^25 tiles
+      if (p.S > 32) sl = s < p.S ? session_len(p, s) : 0;  // else still held from above
+      const int nt = s < p.S ? tiles_of(sl) : 0;
+      int incl = nt;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
         if (lane >= o) incl += up;
       }
-      const long long mine = base + (long long)(incl - nt) * HR;
-      const bool here = s < p.S && (whole ? s == s_whole : (t0 >= mine && t0 < mine + (long long)nt * HR));
+      const int mine = base + (incl - nt) * HR;
+      const bool here = s < p.S && (r.whole ? s == s_whole : (r.t_begin >= mine && r.t_begin < mine + nt * HR));
       const unsigned hit = __ballot_sync(0xFFFFFFFFu, here);
       if (hit) {
         const int src = __ffs(hit) - 1;
         r.s = s0 + src;
         r.base = __shfl_sync(0xFFFFFFFFu, mine, src);
-        if (whole) {
-          const int n = __shfl_sync(0xFFFFFFFFu, nt, src);
-          t0 = r.base + (long long)(c % HR) * n;
-          r.t_end = t0 + n;
+        r.sl = __shfl_sync(0xFFFFFFFFu, sl, src);
+        if (r.whole) {
+          r.t_begin = r.base + (c - s_whole * HR) * tiles_of(r.sl);
+          r.t_end = r.t_begin + tiles_of(r.sl);
         }
         break;
       }
-      base += (long long)__shfl_sync(0xFFFFFFFFu, incl, 31) * HR;
+      base += __shfl_sync(0xFFFFFFFFu, incl, 31) * HR;
     }
-    r.t_begin = t0;
   }
   if (lane == 0) *out = r;
 }
@@ -152,42 +153,39 @@ struct Seg {
   int item, s, g, rg;
   int lo, hi;            // its tiles [lo, hi) of the item's nt
   int sl;                // session length
-  long long item_t0;     // the item's first tile
+  int item_t0;           // the item's first tile
   int nt;
   int row_lo, rows;      // query rows [row_lo, row_lo + rows) of the N*G rows of this KV head
   int i_lo, n_ag;        // agents spanned by them
 };
 
-// Walks a CTA's range segment by segment; every role does so alike.
+// Walks a CTA's range segment by segment.
 struct Walk {
-  long long t, t_end, base;
-  int s, nt, sl;
-  __device__ __forceinline__ void start(const QDecodeParams& p, const Range& r) {
+  int t, t_end, base, s, nt, sl;
+  __device__ __forceinline__ void start(const Range& r) {
     t = r.t_begin;
     t_end = r.t_end;
     base = r.base;
     s = r.s;
-    sl = t < t_end ? session_len(p, s) : 0;
+    sl = r.sl;
     nt = tiles_of(sl);
   }
   __device__ __forceinline__ bool next(const QDecodeParams& p, Seg& sg) {
     if (t >= t_end) return false;
     const int HR = p.Hkv * p.n_rg;
-    while (t >= base + (long long)nt * HR) {
-      base += (long long)nt * HR;
+    while (t >= base + nt * HR) {
+      base += nt * HR;
       sl = session_len(p, ++s);
       nt = tiles_of(sl);
     }
-    const int in = (int)(t - base);  // < nt * HR, checked on the host to fit
-    const int idx = in / nt;
-    sg.lo = in - idx * nt;
-    const long long left = t_end - t;
-    sg.hi = left < nt - sg.lo ? sg.lo + (int)left : nt;
+    const int idx = (t - base) / nt;
+    sg.lo = t - base - idx * nt;
+    sg.hi = min(nt, sg.lo + t_end - t);
     sg.s = s;
     sg.sl = sl;
     sg.nt = nt;
     sg.item = s * HR + idx;
-    sg.item_t0 = base + (long long)idx * nt;
+    sg.item_t0 = base + idx * nt;
     sg.g = idx / p.n_rg;
     sg.rg = idx - sg.g * p.n_rg;
     sg.row_lo = sg.rg * p.rows_per_group;
@@ -206,11 +204,11 @@ struct Walk {
 // it: every contiguous stretch of the order then covers the item evenly, and so
 // does every CTA's share.  A partial last run stays in place.
 struct QOrder {
-  int runs, stride, j, r, w;
-  __device__ __forceinline__ void start(int nt, int k0, bool balance) {
+  int runs, stride;
+  __device__ __forceinline__ void start(int nt, bool balance) {
     runs = nt / kTileRun;
     stride = 1;
-    if (balance && runs > 2) {
+    if (balance && runs > 2 && runs < 65536) {  // j * stride stays within 32 bits
       stride = (int)(0.618f * runs) | 1;
       for (;;) {
         int x = stride, y = runs;
@@ -224,24 +222,10 @@ struct QOrder {
       }
       if (stride >= runs) stride = 1;
     }
-    j = k0 / kTileRun;
-    w = k0 - j * kTileRun;
-    r = j < runs ? (int)((long long)j * stride % runs) : j;
   }
-  __device__ __forceinline__ int tile() const { return r * kTileRun + w; }
-  // the tile k places on
-  __device__ __forceinline__ int ahead(int k) const {
-    const int at = j * kTileRun + w + k, ja = at / kTileRun;
-    return (ja < runs ? (int)((long long)ja * stride % runs) : ja) * kTileRun + at % kTileRun;
-  }
-  __device__ __forceinline__ void next() {
-    if (++w == kTileRun) {
-      w = 0;
-      ++j;
-      r += stride;
-      if (r >= runs) r -= runs;
-      if (j >= runs) r = j;
-    }
+  __device__ __forceinline__ int tile(int k) const {  // the k-th tile visited
+    const int j = k / kTileRun;
+    return (stride > 1 && j < runs ? (int)((unsigned)j * (unsigned)stride % (unsigned)runs) : j) * kTileRun + k % kTileRun;
   }
 };
 
@@ -260,27 +244,28 @@ __device__ __forceinline__ int load_offset(const QDecodeParams& p, int s, int ag
 // ---------------------------------------------------------------------------
 // Tile n of the CTA goes to ring stage n % stages.  Tiles that reach past an offset
 // take a stage of the U ring too; tiles without one then do not hold its space.
-// Three warps produce, each walking the CTA's tiles by itself: one issues the K/V
-// copies, one the U copies, one writes the stages' Meta (a single warp doing it all
-// took 1,400 cycles a tile, twice what a tile takes at the HBM rate).
+// One warp plans: it walks the CTA's tiles, 32 at a time with one lane each, and
+// writes their coordinates, scales and U stages into a table, several chunks ahead.
+// One thread issues the K/V copies and one warp the U copies, reading the table: what
+// stands between two copies is then short.  (One warp that walked, looked up and
+// copied took 1,400 cycles a tile, three that each walked 960; a tile takes 730 at
+// the HBM rate.)
 // The stages of the K/V ring are a multiple of the consumer groups, so a stage always
 // serves one group, which has seen every earlier phase of its barriers.  A U stage
 // serves any group: useq holds the number of its U tile, and a group waits for its own
 // number there before it waits on the barrier, lest an older phase of the same parity
-// satisfy the wait.
+// satisfy the wait.  A stage is released only by warps that saw its bytes land, so a
+// copy is never issued into a stage whose last copy is still landing, abort or not.
 struct QBars {
-  uint64_t *full, *empty, *told, *u_full, *u_empty;  // told: the stage's Meta is written
-  Meta* meta;
+  uint64_t *full, *empty, *u_full, *u_empty;
+  uint64_t *planned, *scaled, *used;  // chunks of the table: coordinates, scales written; every reader done
+  Entry* table;
   volatile int* useq;
   volatile int* abort_flag;
 };
 
-// Wait until a stage is free.  False after an abort: the consumers then release stages
-// without waiting for their copies, so nothing more may be issued.  Warp-uniform.
-__device__ __forceinline__ bool q_wait_free(const QDecodeParams& p, uint64_t* empty, uint32_t phase,
-                                            volatile int* abort_flag) {
-  const bool freed = mbar_wait_bounded(empty, phase ^ 1, abort_flag, p.flags, p.spin_cap, true);
-  return !__any_sync(0xFFFFFFFFu, !freed || *abort_flag);
+__device__ __forceinline__ bool q_wait(const QDecodeParams& p, const QBars& bar, uint64_t* b, uint32_t phase) {
+  return mbar_wait_bounded(b, phase, bar.abort_flag, p.flags, p.spin_cap, true);
 }
 
 // After an abort: wait (bounded) for the copies of the last `issued` stages to land.
@@ -296,182 +281,156 @@ __device__ __forceinline__ void q_drain(uint64_t* full, int stages, int issued, 
   }
 }
 
-template <int D>
-__device__ void q_produce_kv(const QDecodeParams& p, const CUtensorMap* tmK, const CUtensorMap* tmV, uint8_t* smem,
-                             const QDecodeSmem& lay, const QBars& bar, const Range& range) {
+// Chunk c of the table: its barriers' index and phase.
+__device__ __forceinline__ int plan_slot(int n) { return n / kPlan % kPlans; }
+__device__ __forceinline__ uint32_t plan_phase(int n) { return n / (kPlan * kPlans) & 1; }
+
+__device__ __forceinline__ void q_plan(const QDecodeParams& p, const QBars& bar, const Range& range) {
   const int lane = threadIdx.x & 31;
+  const bool paged = p.page_table != nullptr;
+  int n = 0, un = 0;
+  Walk walk;
+  walk.start(range);
+  Seg sg;
+  // the lanes of a chunk are filled segment by segment; `open`: the chunk's slots are ours
+  bool alive = true;
+  auto open = [&] {  // before the first entry of a chunk
+    if (n % kPlan == 0 && n >= kPlan * kPlans)
+      alive = alive && !__any_sync(0xFFFFFFFFu, !q_wait(p, bar, &bar.used[plan_slot(n)], plan_phase(n) ^ 1));
+    return alive;
+  };
+  while (walk.next(p, sg)) {
+    if (sg.sl == 0) continue;  // nothing to read
+    const int tiles = sg.hi - sg.lo;
+    const int my_a = lane < sg.n_ag ? load_offset(p, sg.s, sg.i_lo + lane, false) : 0x7fffffff;
+    const int32_t* pages = p.page_table + (size_t)sg.s * p.pt_stride;
+    QOrder ord;
+    ord.start(sg.nt, p.balance && !range.whole);
+    for (int k = 0; k < tiles;) {
+      if (!open()) return;
+      const int slot = n % kPlan, m = min(kPlan - slot, tiles - k);  // this pass: m tiles
+      Entry* e = bar.table + plan_slot(n) * kPlan + slot + lane;
+      const bool live = lane < m;
+      int tile = 0, c3 = sg.s;
+      bool ok = live;
+      if (live) {
+        tile = ord.tile(sg.lo + k + lane);
+        if (paged) {
+          c3 = __ldg(pages + tile);
+          ok = c3 >= 0 && c3 < p.num_pages;
+          if (!ok) atomicOr(p.flags, LRKV_DEVFLAG_PAGE);
+        }
+      }
+      unsigned need = 0;
+      for (int j = 0; j < sg.n_ag; ++j)
+        need |= (tile + 1) * kQBlock > __shfl_sync(0xFFFFFFFFu, my_a, j) ? 1u << j : 0u;
+      const unsigned with_u = __ballot_sync(0xFFFFFFFFu, live && need);
+      const int my_un = un + __popc(with_u & ((1u << lane) - 1));
+      if (live) {
+        e->key0 = ok ? tile * kQBlock : kBadTile;
+        e->c3 = c3;
+        e->head = sg.g | sg.i_lo << 16;
+        e->session = sg.s;
+        e->u = need ? (int)need | my_un % p.u_stages << 16 | (my_un / p.u_stages & 1) << 24 : 0;
+        e->un = my_un;
+      }
+      un += __popc(with_u);
+      const bool filled = slot + m == kPlan;
+      __syncwarp();
+      if (filled && lane == 0) mbar_arrive(&bar.planned[plan_slot(n)]);
+      if (ok) {
+        const long long at = paged ? c3 * p.s_sp + sg.g * p.s_sh : sg.s * p.s_ss + sg.g * p.s_sh + tile;
+        e->ks = __ldg(p.k_scale + at);
+        e->vs = __ldg(p.v_scale + at);
+      }
+      __syncwarp();
+      if (filled && lane == 0) mbar_arrive(&bar.scaled[plan_slot(n)]);
+      k += m;
+      n += m;
+    }
+  }
+  if (!open()) return;
+  if (lane == 0) {  // the end
+    bar.table[plan_slot(n) * kPlan + n % kPlan].key0 = kNoTile;
+    mbar_arrive(&bar.planned[plan_slot(n)]);
+    mbar_arrive(&bar.scaled[plan_slot(n)]);
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void q_produce_kv(const QDecodeParams& p, const CUtensorMap* tmK, const CUtensorMap* tmV,
+                                             uint8_t* smem, const QDecodeSmem& lay, const QBars& bar) {
   const uint64_t policy = policy_evict_first();
   constexpr int KV_BYTES = kQBlock * D;
   const bool paged = p.page_table != nullptr;
   int stage = 0, n = 0;
   uint32_t phase = 0;
-  bool stop = p.stall != 0;  // the test hook: issue nothing, so the consumers' waits run out
-  Walk walk;
-  walk.start(p, range);
-  Seg sg;
-  while (!stop && walk.next(p, sg)) {
-    if (sg.sl == 0) continue;
-    const int tiles = sg.hi - sg.lo;
-    QOrder ord;
-    ord.start(sg.nt, sg.lo, p.balance && !range.whole);
-    // page ids of 32 tiles, one per lane, and of the 32 after them
-    const int32_t* table = p.page_table + (size_t)sg.s * p.pt_stride;
-    int ids = paged && lane < tiles ? __ldg(table + ord.ahead(lane)) : 0, ids_next = 0;
-    for (int k = 0; k < tiles; ++k, ord.next()) {
-      if (paged && (k & 31) == 0) {
-        if (k > 0) ids = ids_next;
-        ids_next = k + 32 + lane < tiles ? __ldg(table + ord.ahead(32 + lane)) : 0;
-      }
-      const int tile = ord.tile();
-      const int page = __shfl_sync(0xFFFFFFFFu, ids, k & 31);
-      if (!q_wait_free(p, &bar.empty[stage], phase, bar.abort_flag)) {
-        stop = true;
-        break;
-      }
-      if (lane == 0) {
-        uint64_t* full = &bar.full[stage];
-        if (paged && (page < 0 || page >= p.num_pages)) {
-          atomicOr(p.flags, LRKV_DEVFLAG_PAGE);
-          mbar_arrive(full);
-        } else {
-          uint8_t* st = smem + stage * lay.tile_bytes;
-          const int c1 = paged ? 0 : tile * kQBlock, c3 = paged ? page : sg.s;
-          mbar_arrive_expect_tx(full, 2 * KV_BYTES);
-          tma_load_4d(st, tmK, full, 0, c1, sg.g, c3, policy);
-          tma_load_4d(st + KV_BYTES, tmV, full, 0, c1, sg.g, c3, policy);
-        }
-      }
-      __syncwarp();
-      ++n;
-      if (++stage == p.stages) {
-        stage = 0;
-        phase ^= 1;
-      }
+  for (;; ++n) {
+    if (n % kPlan == 0) {
+      if (n > 0) mbar_arrive(&bar.used[plan_slot(n - 1)]);
+      if (!q_wait(p, bar, &bar.planned[plan_slot(n)], plan_phase(n))) break;
+    }
+    const int4 e = *reinterpret_cast<const int4*>(&bar.table[plan_slot(n) * kPlan + n % kPlan]);
+    if (e.x == kNoTile) break;
+    if (!q_wait(p, bar, &bar.empty[stage], phase ^ 1)) break;
+    uint64_t* full = &bar.full[stage];
+    if (e.x == kBadTile) {
+      mbar_arrive(full);
+    } else {
+      uint8_t* st = smem + stage * lay.tile_bytes;
+      const int c1 = paged ? 0 : e.x, g = e.z & 0xFFFF;
+      mbar_arrive_expect_tx(full, 2 * KV_BYTES);
+      tma_load_4d(st, tmK, full, 0, c1, g, e.y, policy);
+      tma_load_4d(st + KV_BYTES, tmV, full, 0, c1, g, e.y, policy);
+    }
+    if (++stage == p.stages) {
+      stage = 0;
+      phase ^= 1;
     }
   }
   // no copy of this CTA may still be landing in shared memory when it exits
-  if (*bar.abort_flag && lane == 0) q_drain(bar.full, p.stages, n, stage, phase);
+  if (*bar.abort_flag) q_drain(bar.full, p.stages, n, stage, phase);
 }
 
 template <int RK>
 __device__ void q_produce_u(const QDecodeParams& p, const CUtensorMap* tmU, uint8_t* smem, const QDecodeSmem& lay,
-                            const QBars& bar, const Range& range) {
+                            const QBars& bar) {
   const int lane = threadIdx.x & 31;
   const uint64_t policy = policy_evict_last();
   constexpr int U_BYTES = kQBlock * RK * 2;
   const bool per_agent = p.mode == LRKV_BASE_SHARED;
   int us = 0, un = 0;
   uint32_t phase = 0;
-  bool stop = p.stall != 0;
-  Walk walk;
-  walk.start(p, range);
-  Seg sg;
-  while (!stop && walk.next(p, sg)) {
-    if (sg.sl == 0) continue;
-    const int my_a = lane < sg.n_ag ? load_offset(p, sg.s, sg.i_lo + lane, false) : 0x7fffffff;
-    QOrder ord;
-    ord.start(sg.nt, sg.lo, p.balance && !range.whole);
-    for (int k = 0; k < sg.hi - sg.lo; ++k, ord.next()) {
-      const int key0 = ord.tile() * kQBlock;
-      const unsigned need = __ballot_sync(0xFFFFFFFFu, key0 + kQBlock > my_a);
-      if (!need) continue;
-      if (!q_wait_free(p, &bar.u_empty[us], phase, bar.abort_flag)) {
-        stop = true;
-        break;
-      }
-      uint64_t* full = &bar.u_full[us];
-      if (lane == 0) {
-        bar.useq[us] = un;
-        mbar_arrive_expect_tx(full, (per_agent ? __popc(need) : 1) * U_BYTES);
-      }
+  for (int n = 0;; ++n) {
+    if (n % kPlan == 0) {
       __syncwarp();
-      if (per_agent ? (need >> lane & 1) : lane == 0)  // one agent's tile per lane
-        tma_load_4d(smem + lay.u_off + us * lay.u_bytes + lane * U_BYTES, tmU, full, 0, key0,
-                    per_agent ? sg.i_lo + lane : 0, sg.s, policy);
-      ++un;
-      if (++us == p.u_stages) {
-        us = 0;
-        phase ^= 1;
-      }
+      if (n > 0 && lane == 0) mbar_arrive(&bar.used[plan_slot(n - 1)]);
+      if (__any_sync(0xFFFFFFFFu, !q_wait(p, bar, &bar.planned[plan_slot(n)], plan_phase(n)))) break;
+    }
+    const Entry* e = &bar.table[plan_slot(n) * kPlan + n % kPlan];
+    const int key0 = e->key0;
+    if (key0 == kNoTile) break;
+    const unsigned need = e->u & 0xFFFF;
+    if (!need) continue;
+    if (__any_sync(0xFFFFFFFFu, !q_wait(p, bar, &bar.u_empty[us], phase ^ 1))) break;
+    uint64_t* full = &bar.u_full[us];
+    if (lane == 0) {
+      bar.useq[us] = un;
+      if (key0 < 0) mbar_arrive(full);
+      else mbar_arrive_expect_tx(full, (per_agent ? __popc(need) : 1) * U_BYTES);
+    }
+    __syncwarp();
+    if (key0 >= 0 && (per_agent ? (need >> lane & 1) : lane == 0))  // one agent's tile per lane
+      tma_load_4d(smem + lay.u_off + us * lay.u_bytes + lane * U_BYTES, tmU, full, 0, key0,
+                  per_agent ? (e->head >> 16) + lane : 0, e->session, policy);
+    ++un;
+    if (++us == p.u_stages) {
+      us = 0;
+      phase ^= 1;
     }
   }
   __syncwarp();
   if (*bar.abort_flag && lane == 0) q_drain(bar.u_full, p.u_stages, un, us, phase);
-}
-
-__device__ __forceinline__ void q_produce_meta(const QDecodeParams& p, const QBars& bar, const Range& range) {
-  const int lane = threadIdx.x & 31;
-  const bool paged = p.page_table != nullptr;
-  int stage = 0, us = 0, un = 0;
-  uint32_t phase = 0, uphase = 0;
-  bool stop = p.stall != 0;
-  Walk walk;
-  walk.start(p, range);
-  Seg sg;
-  while (!stop && walk.next(p, sg)) {
-    if (sg.sl == 0) continue;
-    const int tiles = sg.hi - sg.lo;
-    const int my_a = lane < sg.n_ag ? load_offset(p, sg.s, sg.i_lo + lane, false) : 0x7fffffff;
-    const int a_min = __reduce_min_sync(0xFFFFFFFFu, my_a);
-    QOrder ord;
-    ord.start(sg.nt, sg.lo, p.balance && !range.whole);
-    const int32_t* table = p.page_table + (size_t)sg.s * p.pt_stride;
-    const long long dense = sg.s * p.s_ss + sg.g * p.s_sh, head = sg.g * p.s_sh;
-    // one lane per tile of a run of 32: its place in the cache (page, or tile), its
-    // scales; the next run's are fetched while this one is written
-    auto fetch = [&](int where, float& ks, float& vs) {
-      const bool ok = where >= 0 && (!paged || where < p.num_pages);
-      const long long at = paged ? where * p.s_sp + head : dense + where;
-      ks = ok ? __ldg(p.k_scale + at) : 0.f;
-      vs = ok ? __ldg(p.v_scale + at) : 0.f;
-      return ok;
-    };
-    int where = lane < tiles ? (paged ? __ldg(table + ord.ahead(lane)) : ord.ahead(lane)) : -1, where_next = -1;
-    float ks, vs, ks_next = 0.f, vs_next = 0.f;
-    bool ok = fetch(where, ks, vs), ok_next = false;
-    for (int k = 0; k < tiles; ++k, ord.next()) {
-      const int in = k & 31;
-      if (in == 0) {
-        if (k > 0) {
-          ks = ks_next;
-          vs = vs_next;
-          ok = ok_next;
-        }
-        const int ahead = ord.ahead(32 + lane);
-        where_next = k + 32 + lane < tiles ? (paged ? __ldg(table + ahead) : ahead) : -1;
-      } else if (in == 16) {
-        ok_next = fetch(where_next, ks_next, vs_next);
-      }
-      const int key0 = ord.tile() * kQBlock;
-      const bool has_u = key0 + kQBlock > a_min;
-      if (!q_wait_free(p, &bar.empty[stage], phase, bar.abort_flag)) {
-        stop = true;
-        break;
-      }
-      if (lane == in) {
-        Meta* m = &bar.meta[stage];
-        m->ks = ks;
-        m->vs = vs;
-        m->key0 = ok ? key0 : -1;
-        m->us = has_u ? us : -1;
-        m->un = un;
-        m->uphase = uphase;
-        mbar_arrive(&bar.told[stage]);
-      }
-      __syncwarp();
-      if (++stage == p.stages) {
-        stage = 0;
-        phase ^= 1;
-      }
-      if (has_u) {
-        ++un;
-        if (++us == p.u_stages) {
-          us = 0;
-          uphase ^= 1;
-        }
-      }
-    }
-  }
 }
 
 // ---------------------------------------------------------------------------
@@ -918,8 +877,8 @@ __device__ __forceinline__ void q_sync() { named_bar_sync(1, kQThreads); }
 
 // Two records per CTA: 0 for the segment that starts the CTA's range, 1 for a later
 // one (only its last can be shared with the next CTA).
-__device__ __forceinline__ size_t q_record_slot(long long cta, long long cta_begin, long long item_t0) {
-  return 2 * cta + (item_t0 > cta_begin ? 1 : 0);
+__device__ __forceinline__ size_t q_record_slot(int cta, int cta_begin, int item_t0) {
+  return 2 * (size_t)cta + (item_t0 > cta_begin ? 1 : 0);
 }
 
 // Merge the warps' rows into the CTA's record rec = [m | l | O | Z] in shared
@@ -931,7 +890,7 @@ __device__ __forceinline__ void merge_warps(WarpRows<D, RK, H16, H8>& st, float*
   using WR = WarpRows<D, RK, H16, H8>;
   constexpr int RPW = WR::RPW, RP = RPW * NRB, NR = WR::NR, R8 = WR::R8;
   constexpr int PEERS = kQWarps / NRB;
-  constexpr int CW = kQMergeCols;
+  constexpr int CW = kQMergeCols, LD = kQMergeLd;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
   int row[NR];  // this lane's rows within the block
 #pragma unroll
@@ -972,18 +931,18 @@ __device__ __forceinline__ void merge_warps(WarpRows<D, RK, H16, H8>& st, float*
     rec[tid] = M;
     rec[RP + tid] = L;
   }
-  float* mine = mb + (peer * NRB + rb) * RPW * CW;
+  float* mine = mb + (peer * NRB + rb) * RPW * LD;
   float* mO = rec + 2 * RP;
   float* mZ = mO + RP * D;
   auto reduce = [&](float* dst, int ld, int width) {  // dst[row][0 .. width) = sum over the peers
     q_sync();
     for (int e = 2 * tid; e < RP * width; e += 2 * kQThreads) {
       const int r = e / width, col = e - r * width;
-      const float* src = mb + ((r / RPW) * RPW + r % RPW) * CW + col;
+      const float* src = mb + ((r / RPW) * RPW + r % RPW) * LD + col;
       float2 a = make_float2(0.f, 0.f);
 #pragma unroll
       for (int x = 0; x < PEERS; ++x) {
-        const float2 v = *reinterpret_cast<const float2*>(src + x * NRB * RPW * CW);
+        const float2 v = *reinterpret_cast<const float2*>(src + x * NRB * RPW * LD);
         a.x += v.x;
         a.y += v.y;
       }
@@ -999,7 +958,7 @@ __device__ __forceinline__ void merge_warps(WarpRows<D, RK, H16, H8>& st, float*
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const float* o = st.o16[c0 / 8 + x];
-          *reinterpret_cast<float2*>(mine + row[i] * CW + 8 * x + 2 * t4) =
+          *reinterpret_cast<float2*>(mine + row[i] * LD + 8 * x + 2 * t4) =
               make_float2(o[2 * i] * fo[i] * fo[i], o[2 * i + 1] * fo[i] * fo[i]);
         }
     }
@@ -1009,7 +968,7 @@ __device__ __forceinline__ void merge_warps(WarpRows<D, RK, H16, H8>& st, float*
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int i = R8 + (e & 1);
-          mine[row[i] * CW + 16 * x + 8 * (e >> 1) + g8] = st.o8[c0 / 16 + x][e] * fo[i] * fo[i];
+          mine[row[i] * LD + 16 * x + 8 * (e >> 1) + g8] = st.o8[c0 / 16 + x][e] * fo[i] * fo[i];
         }
     }
     reduce(mO + c0, D, CW);
@@ -1024,7 +983,7 @@ __device__ __forceinline__ void merge_warps(WarpRows<D, RK, H16, H8>& st, float*
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         if (16 * mz + 8 * (e >> 1) < RK)
-          mine[(8 * x + 2 * t4 + (e & 1)) * CW + 16 * mz + 8 * (e >> 1) + g8] = st.z[x][mz][e] * (e & 1 ? f1 : f0);
+          mine[(8 * x + 2 * t4 + (e & 1)) * LD + 16 * mz + 8 * (e >> 1) + g8] = st.z[x][mz][e] * (e & 1 ? f1 : f0);
   }
   reduce(mZ, RK, RK);
 }
@@ -1037,14 +996,14 @@ __device__ __forceinline__ void finish_item(const QDecodeParams& p, const Range&
   constexpr int REC = RP * (D + RK + 2);
   constexpr int E4 = RP * (D + RK) / 4;
   constexpr int PER = (E4 + kQThreads - 1) / kQThreads;
-  constexpr int TABLE = kQWarps * (RP > 16 && RP != 24 ? 16 : RP) * kQMergeCols;  // floats of the merge buffer
+  constexpr int TABLE = kQWarps * (RP > 16 && RP != 24 ? 16 : RP) * kQMergeLd;  // floats of the merge buffer
   constexpr int CHUNK = TABLE / RP / 2;                                           // records whose m and l it holds
   const int tid = threadIdx.x;
   const bool shared = !range.whole && (sg.lo > 0 || sg.hi < sg.nt);
   if (shared) {
-    const long long C = range.ctas, W = range.W;
-    const long long c_first = owner_cta(sg.item_t0, W, C), c_last = owner_cta(sg.item_t0 + sg.nt - 1, W, C);
-    const int segs = (int)(c_last - c_first + 1);
+    const int C = range.ctas, W = range.W;
+    const int c_first = (int)owner_cta(sg.item_t0, W, C), c_last = (int)owner_cta(sg.item_t0 + sg.nt - 1, W, C);
+    const int segs = c_last - c_first + 1;
     float* mine = p.partials + q_record_slot(blockIdx.x, range.t_begin, sg.item_t0) * REC;
     for (int e = 4 * tid; e < REC; e += 4 * kQThreads)
       __stcg(reinterpret_cast<float4*>(mine + e), *reinterpret_cast<const float4*>(rec + e));
@@ -1059,7 +1018,7 @@ __device__ __forceinline__ void finish_item(const QDecodeParams& p, const Range&
     if (!*bcast) return;
     __threadfence();
     // Only the item's first CTA can hold it in its second record slot.
-    const float* first = p.partials + q_record_slot(c_first, c_first * W / C, sg.item_t0) * REC;
+    const float* first = p.partials + q_record_slot(c_first, range_begin(c_first, W, C), sg.item_t0) * REC;
     const float* rest = p.partials + 2 * (size_t)c_first * REC;
     auto record = [&](int j) { return j == 0 ? first : rest + (size_t)(2 * j) * REC; };
     float4 acc[PER];
@@ -1182,17 +1141,17 @@ __device__ __forceinline__ void finish_item(const QDecodeParams& p, const Range&
 }
 
 // Wait until a U stage holds U tile number un, then for its bytes.
-__device__ __forceinline__ void q_wait_u(const QDecodeParams& p, const QBars& bar, int us, int un, uint32_t phase) {
+__device__ __forceinline__ bool q_wait_u(const QDecodeParams& p, const QBars& bar, int us, int un, uint32_t phase) {
   uint32_t spins = 0;
   while (bar.useq[us] != un) {
-    if (*bar.abort_flag) break;
+    if (*bar.abort_flag) return false;
     if (++spins >= p.spin_cap) {
       *bar.abort_flag = 1;
       atomicOr(p.flags, LRKV_DEVFLAG_TIMEOUT);
-      break;
+      return false;
     }
   }
-  mbar_wait_bounded(&bar.u_full[us], phase, bar.abort_flag, p.flags, p.spin_cap, true);
+  return q_wait(p, bar, &bar.u_full[us], phase);
 }
 
 template <int FMT, int D, int RK, int H16, int H8, int NRB>
@@ -1213,10 +1172,11 @@ __device__ void q_consumers(const QDecodeParams& p, uint8_t* smem, const QDecode
   int* a_sm = reinterpret_cast<int*>(smem + lay.a_off);
   const uint32_t ring = smem_u32(smem);
   // the group's next tile (number, stage, phase); the CTA's tiles before this segment
-  int n = og, stage = og % p.stages, before = 0;
-  uint32_t phase = (og / p.stages) & 1;
+  int n = og, stage = og, before = 0;
+  uint32_t phase = 0;
+  bool alive = true;  // until a wait gives up: then nothing is read or released any more
   Walk walk;
-  walk.start(p, range);
+  walk.start(range);
   Seg sg;
   WR st;
   while (walk.next(p, sg)) {
@@ -1252,21 +1212,36 @@ __device__ void q_consumers(const QDecodeParams& p, uint8_t* smem, const QDecode
       for (int mz = 0; mz < WR::MZ; ++mz) st.z[x][mz][0] = st.z[x][mz][1] = st.z[x][mz][2] = st.z[x][mz][3] = 0.f;
 
     before += sg.sl > 0 ? sg.hi - sg.lo : 0;  // an empty session has no tiles
-    while (n < before) {
-      mbar_wait_bounded(&bar.told[stage], phase, bar.abort_flag, p.flags, p.spin_cap, true);
-      const Meta* meta = bar.meta + stage;
-      const float2 scales = *reinterpret_cast<const float2*>(meta);
-      const int key0 = meta->key0, us = meta->us;
-      mbar_wait_bounded(&bar.full[stage], phase, bar.abort_flag, p.flags, p.spin_cap, true);
-      const bool last = key0 + kQBlock > sg.sl;
+    while (alive && n < before) {
+      // the group's tiles of a chunk of the table are n % kPlan = og, og + NG, ..
+      const int slot = plan_slot(n);
+      if (n % kPlan < NG && __any_sync(0xFFFFFFFFu, !q_wait(p, bar, &bar.scaled[slot], plan_phase(n)))) {
+        alive = false;
+        break;
+      }
+      const Entry* e = &bar.table[slot * kPlan + n % kPlan];
+      const int key0 = e->key0, u = e->u, un = e->un;
+      const float ks = e->ks, vs = e->vs;
+      if (__any_sync(0xFFFFFFFFu, !q_wait(p, bar, &bar.full[stage], phase))) {
+        alive = false;
+        break;
+      }
       uint32_t pz[NB][WR::OCT][2];
       const uint32_t Ks = ring + stage * lay.tile_bytes;
-      if (key0 >= 0) {
-        q_tile<FMT, D, RK, H16, H8>(st, sg.sl, Ks, scales.x, scales.y, key0, kw, qs, us >= 0, pz);
+      if (key0 >= 0) q_tile<FMT, D, RK, H16, H8>(st, sg.sl, Ks, ks, vs, key0, kw, qs, u != 0, pz);
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&bar.empty[stage]);
+        if (n % kPlan >= kPlan - NG) mbar_arrive(&bar.used[slot]);  // its last tile of the chunk
       }
-      if (us >= 0) {
-        q_wait_u(p, bar, us, meta->un, meta->uphase);
+      if (u) {
+        const int us = u >> 16 & 0xFF;
+        if (__any_sync(0xFFFFFFFFu, !q_wait_u(p, bar, us, un, u >> 24))) {
+          alive = false;
+          break;
+        }
         if (key0 >= 0) {
+          const bool last = key0 + kQBlock > sg.sl;
           const bool one_pass = p.mode == LRKV_BASE_LR_SHARED && !last && a_max <= key0;
           const unsigned mine = __ballot_sync(0xFFFFFFFFu, lane >= ag_lo && lane <= ag_hi && key0 + kQBlock > lane_a);
           const bool clean = !last && !__any_sync(0xFFFFFFFFu, (mine >> lane & 1) && lane_a > key0);
@@ -1278,12 +1253,10 @@ __device__ void q_consumers(const QDecodeParams& p, uint8_t* smem, const QDecode
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.u_empty[us]);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.empty[stage]);
       n += NG;
       stage += NG;
-      while (stage >= p.stages) {
-        stage -= p.stages;
+      if (stage >= p.stages) {
+        stage = og;
         phase ^= 1;
       }
     }
@@ -1310,10 +1283,12 @@ __global__ void __launch_bounds__(kQBlockThreads, 1)
   QBars bar;
   bar.full = reinterpret_cast<uint64_t*>(smem + lay.bar_off);
   bar.empty = bar.full + p.stages;
-  bar.told = bar.empty + p.stages;
-  bar.u_full = bar.told + p.stages;
+  bar.u_full = bar.empty + p.stages;
   bar.u_empty = bar.u_full + p.u_stages;
-  bar.meta = reinterpret_cast<Meta*>(smem + lay.meta_off);
+  bar.planned = bar.u_empty + p.u_stages;
+  bar.scaled = bar.planned + kPlans;
+  bar.used = bar.scaled + kPlans;
+  bar.table = reinterpret_cast<Entry*>(smem + lay.plan_off);
   bar.useq = reinterpret_cast<volatile int*>(smem + lay.useq_off);
   Range* range = reinterpret_cast<Range*>(smem + lay.misc_off);
   bar.abort_flag = reinterpret_cast<volatile int*>(range + 1);
@@ -1323,13 +1298,17 @@ __global__ void __launch_bounds__(kQBlockThreads, 1)
     constexpr int READERS = kQBlock / kQWarpKeys * NRB;  // warps that read a tile
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&bar.full[s], 1);
-      mbar_init(&bar.told[s], 1);
       mbar_init(&bar.empty[s], READERS);
     }
     for (int s = 0; s < p.u_stages; ++s) {
       mbar_init(&bar.u_full[s], 1);
       mbar_init(&bar.u_empty[s], READERS);
       bar.useq[s] = -1;
+    }
+    for (int s = 0; s < kPlans; ++s) {
+      mbar_init(&bar.planned[s], 1);
+      mbar_init(&bar.scaled[s], 1);
+      mbar_init(&bar.used[s], kQWarps + 2);              // the consumers and the two copying warps
     }
     *bar.abort_flag = 0;
     *bcast = 0;
@@ -1345,9 +1324,14 @@ __global__ void __launch_bounds__(kQBlockThreads, 1)
   const Range r = *range;
   if (warp >= kQWarps) {
     setmaxnreg_dec<kQProducerRegs>();
-    if (warp == kQWarps) q_produce_kv<D>(p, &tmK, &tmV, smem, lay, bar, r);
-    else if (warp == kQWarps + 1) q_produce_u<RK>(p, &tmU, smem, lay, bar, r);
-    else if (warp == kQWarps + 2) q_produce_meta(p, bar, r);
+    // the test hook (p.stall): nothing is copied, so the consumers' waits run out
+    if (warp == kQWarps + 2) {
+      q_plan(p, bar, r);
+    } else if (warp == kQWarps && !p.stall) {
+      if ((threadIdx.x & 31) == 0) q_produce_kv<D>(p, &tmK, &tmV, smem, lay, bar);
+    } else if (warp == kQWarps + 1 && !p.stall) {
+      q_produce_u<RK>(p, &tmU, smem, lay, bar);
+    }
   } else {
     setmaxnreg_inc<kQConsumerRegs>();
     q_consumers<FMT, D, RK, H16, H8, NRB>(p, smem, lay, bar, bcast, r);

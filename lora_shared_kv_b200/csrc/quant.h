@@ -94,10 +94,12 @@ __host__ __device__ constexpr int q_groups(int nrb) { return kQWarps / (kQBlock 
 
 // Columns of O that the warps exchange per pass when their rows are merged.
 constexpr int kQMergeCols = 32;
+constexpr int kQMergeLd = kQMergeCols + 8;  // row stride: four rows' float2 writes lie in different banks
+constexpr int kQPlanBytes = 4 * 32 * 32, kQPlanBarriers = 12;  // the planner's table of tiles
 
 // Shared-memory plan (bytes from a 1024-aligned base).
 struct QDecodeSmem {
-  int tile_bytes, u_bytes, u_off, rec_off, mb_off, ml_off, q_off, meta_off, a_off, bar_off, useq_off, misc_off, total;
+  int tile_bytes, u_bytes, u_off, rec_off, mb_off, ml_off, q_off, plan_off, a_off, bar_off, useq_off, misc_off, total;
 };
 
 __host__ __device__ inline QDecodeSmem q_smem_plan(int D, int RK, int rows_block, int nrb, int n_u_slots, int stages,
@@ -109,12 +111,12 @@ __host__ __device__ inline QDecodeSmem q_smem_plan(int D, int RK, int rows_block
   s.u_off = stages * s.tile_bytes;
   s.rec_off = s.u_off + u_stages * s.u_bytes;                            // [m | l | O | Z] of RP rows
   s.mb_off = s.rec_off + RP * (D + RK + 2) * 4;                          // the warps' columns being merged
-  s.ml_off = s.mb_off + kQWarps * rows_block * kQMergeCols * 4;          // the warps' m and l
+  s.ml_off = s.mb_off + kQWarps * rows_block * kQMergeLd * 4;            // the warps' m and l
   s.q_off = round_up(s.ml_off + kQWarps * rows_block * 2 * 4, 16);       // 24-row blocks: query fragments
-  s.meta_off = s.q_off + (rows_block == 24 ? 24 * D * 2 : 0);            // what the producer tells of each stage
-  s.a_off = s.meta_off + stages * 32;                                    // offsets of the item's agents
+  s.plan_off = s.q_off + (rows_block == 24 ? 24 * D * 2 : 0);            // the planner's table
+  s.a_off = s.plan_off + kQPlanBytes;                                    // offsets of the item's agents
   s.bar_off = round_up(s.a_off + kMaxAgents * 4, 16);
-  s.useq_off = s.bar_off + (3 * stages + 2 * u_stages) * 8;                 // tile number of each U stage
+  s.useq_off = s.bar_off + (2 * (stages + u_stages) + kQPlanBarriers) * 8;                 // tile number of each U stage
   s.misc_off = round_up(s.useq_off + u_stages * 4, 16);                  // the CTA's range, abort word, broadcast word
   s.total = s.misc_off + 96;
   return s;
@@ -125,7 +127,7 @@ inline size_t q_record_floats(int RP, int D, int RK) { return (size_t)RP * (D + 
 // A CTA takes whole items, one each, when there are no more items than CTAs and
 // the longest item is at most `slack` tiles above the even share: nothing is
 // then published or merged.
-__host__ __device__ inline bool q_whole_items(long long items, long long ctas, long long nt_max, long long W, int slack) {
+__host__ __device__ inline bool q_whole_items(int items, int ctas, int nt_max, int W, int slack) {
   return items <= ctas && nt_max <= (W + ctas - 1) / ctas + slack;
 }
 

@@ -120,7 +120,7 @@ lrkv_status plan_decode_quant(const lrkv_problem* p, int max_seq_len, const Devi
   pl->nt = max_seq_len > 0 ? (int)(((long long)max_seq_len + LRKV_QUANT_BLOCK - 1) / LRKV_QUANT_BLOCK) : 1;
   const long long per_session = (long long)p->num_kv_heads * pl->n_rg;
   pl->items = p->num_sessions * per_session;
-  if (pl->items > 0x3FFFFFFF || per_session * pl->nt > 0x7FFFFFFF)
+  if (pl->items > 0x3FFFFFFF || pl->items * pl->nt > 0x7FFF0000)
     return fail(LRKV_ERR_UNSUPPORTED, "too many (session, KV head, row group) items or tiles");
   const int sms = dev.sms > 0 ? dev.sms : 148;
   const long long W = pl->items * pl->nt;
