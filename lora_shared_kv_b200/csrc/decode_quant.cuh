@@ -48,7 +48,6 @@ namespace lrkv {
 namespace {
 
 constexpr float kNegInf = -INFINITY;
-constexpr int kMergeBatch = 4;  // partial records whose loads are in flight together
 
 // The CTA's share of the work, found by warp 0.  Tiles of a launch are counted in 32
 // bits (checked on the host).
@@ -73,7 +72,7 @@ struct __align__(16) Entry {
   int session;
   float ks, vs;  // the block's scales
   int u;         // agents whose U tile is copied (16 bits) | U stage << 16 | its phase << 24; 0: none
-  int un;        // number of the U tile among the CTA's
+  int n;         // number of the tile among the CTA's
 };
 constexpr int kBadTile = -1, kNoTile = -2;
 constexpr int kPlan = 32;   // tiles of a planned chunk
@@ -251,10 +250,11 @@ __device__ __forceinline__ int load_offset(const QDecodeParams& p, int s, int ag
 // copied took 1,400 cycles a tile, three that each walked 960; a tile takes 730 at
 // the HBM rate.)
 // The stages of the K/V ring are a multiple of the consumer groups, so a stage always
-// serves one group, which has seen every earlier phase of its barriers.  A U stage
-// serves any group: useq holds the number of its U tile, and a group waits for its own
-// number there before it waits on the barrier, lest an older phase of the same parity
-// satisfy the wait.  A stage is released only by warps that saw its bytes land, so a
+// serves one group, which has seen every earlier phase of its barriers.  U stage g
+// serves the groups that are g modulo their number; where several groups share one
+// (large U tiles), useq holds the number of the stage's tile, and a group waits for
+// its own tile's there before it waits on the barrier, lest an older phase of the same
+// parity satisfy the wait.  A stage is released only by warps that saw its bytes land, so a
 // copy is never issued into a stage whose last copy is still landing, abort or not.
 struct QBars {
   uint64_t *full, *empty, *u_full, *u_empty;
@@ -285,10 +285,12 @@ __device__ __forceinline__ void q_drain(uint64_t* full, int stages, int issued, 
 __device__ __forceinline__ int plan_slot(int n) { return n / kPlan % kPlans; }
 __device__ __forceinline__ uint32_t plan_phase(int n) { return n / (kPlan * kPlans) & 1; }
 
+template <int NG>
 __device__ __forceinline__ void q_plan(const QDecodeParams& p, const QBars& bar, const Range& range) {
   const int lane = threadIdx.x & 31;
   const bool paged = p.page_table != nullptr;
-  int n = 0, un = 0;
+  int n = 0;
+  int uses = 0;  // lane u: how often U stage u was taken so far
   Walk walk;
   walk.start(range);
   Seg sg;
@@ -324,17 +326,24 @@ __device__ __forceinline__ void q_plan(const QDecodeParams& p, const QBars& bar,
       unsigned need = 0;
       for (int j = 0; j < sg.n_ag; ++j)
         need |= (tile + 1) * kQBlock > __shfl_sync(0xFFFFFFFFu, my_a, j) ? 1u << j : 0u;
-      const unsigned with_u = __ballot_sync(0xFFFFFFFFu, live && need);
-      const int my_un = un + __popc(with_u & ((1u << lane) - 1));
+      // the U stage of tile n + lane, and how often it was taken before
+      const int us = (n + lane) % NG % p.u_stages;
+      unsigned earlier = 0, same = 0;
+      for (int u = 0; u < p.u_stages; ++u) {
+        const unsigned takers = __ballot_sync(0xFFFFFFFFu, live && need && us == u);
+        if (us == u) earlier = takers & ((1u << lane) - 1);
+        if (lane == u) same = takers;
+      }
+      const int use = __shfl_sync(0xFFFFFFFFu, uses, us) + __popc(earlier);
+      uses += __popc(same);
       if (live) {
         e->key0 = ok ? tile * kQBlock : kBadTile;
         e->c3 = c3;
         e->head = sg.g | sg.i_lo << 16;
         e->session = sg.s;
-        e->u = need ? (int)need | my_un % p.u_stages << 16 | (my_un / p.u_stages & 1) << 24 : 0;
-        e->un = my_un;
+        e->u = need ? (int)need | us << 16 | (use & 1) << 24 : 0;
+        e->n = n + lane;
       }
-      un += __popc(with_u);
       const bool filled = slot + m == kPlan;
       __syncwarp();
       if (filled && lane == 0) mbar_arrive(&bar.planned[plan_slot(n)]);
@@ -399,8 +408,7 @@ __device__ void q_produce_u(const QDecodeParams& p, const CUtensorMap* tmU, uint
   const uint64_t policy = policy_evict_last();
   constexpr int U_BYTES = kQBlock * RK * 2;
   const bool per_agent = p.mode == LRKV_BASE_SHARED;
-  int us = 0, un = 0;
-  uint32_t phase = 0;
+  unsigned issued = 0, phases = 0;  // bit u: stage u was filled; the phase of its last filling
   for (int n = 0;; ++n) {
     if (n % kPlan == 0) {
       __syncwarp();
@@ -408,14 +416,16 @@ __device__ void q_produce_u(const QDecodeParams& p, const CUtensorMap* tmU, uint
       if (__any_sync(0xFFFFFFFFu, !q_wait(p, bar, &bar.planned[plan_slot(n)], plan_phase(n)))) break;
     }
     const Entry* e = &bar.table[plan_slot(n) * kPlan + n % kPlan];
-    const int key0 = e->key0;
+    const int key0 = e->key0, u = e->u;
     if (key0 == kNoTile) break;
-    const unsigned need = e->u & 0xFFFF;
-    if (!need) continue;
+    if (!u) continue;
+    const unsigned need = u & 0xFFFF, us = u >> 16 & 0xFF, phase = u >> 24;
     if (__any_sync(0xFFFFFFFFu, !q_wait(p, bar, &bar.u_empty[us], phase ^ 1))) break;
+    issued |= 1u << us;
+    phases = (phases & ~(1u << us)) | phase << us;
     uint64_t* full = &bar.u_full[us];
     if (lane == 0) {
-      bar.useq[us] = un;
+      bar.useq[us] = n;
       if (key0 < 0) mbar_arrive(full);
       else mbar_arrive_expect_tx(full, (per_agent ? __popc(need) : 1) * U_BYTES);
     }
@@ -423,14 +433,10 @@ __device__ void q_produce_u(const QDecodeParams& p, const CUtensorMap* tmU, uint
     if (key0 >= 0 && (per_agent ? (need >> lane & 1) : lane == 0))  // one agent's tile per lane
       tma_load_4d(smem + lay.u_off + us * lay.u_bytes + lane * U_BYTES, tmU, full, 0, key0,
                   per_agent ? (e->head >> 16) + lane : 0, e->session, policy);
-    ++un;
-    if (++us == p.u_stages) {
-      us = 0;
-      phase ^= 1;
-    }
   }
   __syncwarp();
-  if (*bar.abort_flag && lane == 0) q_drain(bar.u_full, p.u_stages, un, us, phase);
+  if (*bar.abort_flag && lane < p.u_stages && (issued >> lane & 1))
+    q_drain(&bar.u_full[lane], 1, 1, 0, (phases >> lane & 1) ^ 1);
 }
 
 // ---------------------------------------------------------------------------
@@ -882,15 +888,18 @@ __device__ __forceinline__ size_t q_record_slot(int cta, int cta_begin, int item
 }
 
 // Merge the warps' rows into the CTA's record rec = [m | l | O | Z] in shared
-// memory.  The warps of a row block held the same rows over different keys; sums
-// run in warp order, so the result does not depend on timing.
+// memory.  The warps of a row block held the same rows over different keys, in the
+// same fragment layout: they exchange whole fragments (a float4 a lane, no index
+// arithmetic while the accumulators are live), a few at a time, and whoever sums one
+// writes it to its place.  Sums run in warp order, so the result does not depend on
+// timing.
 template <int D, int RK, int H16, int H8, int NRB>
-__device__ __forceinline__ void merge_warps(WarpRows<D, RK, H16, H8>& st, float* rec, float* mb, float* ml, int rb,
+__device__ __forceinline__ void merge_warps(WarpRows<D, RK, H16, H8>& st, float* rec, float4* mb, float* ml, int rb,
                                             int peer) {
   using WR = WarpRows<D, RK, H16, H8>;
-  constexpr int RPW = WR::RPW, RP = RPW * NRB, NR = WR::NR, R8 = WR::R8;
+  constexpr int RPW = WR::RPW, RP = RPW * NRB, NR = WR::NR, R8 = WR::R8, MZ = WR::MZ;
   constexpr int PEERS = kQWarps / NRB;
-  constexpr int CW = kQMergeCols, LD = kQMergeLd;
+  constexpr int N16 = H16 ? D / 8 : 0, N8 = H8 ? D / 16 : 0, NF = N16 + N8 + WR::OCT * MZ;  // fragments
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
   int row[NR];  // this lane's rows within the block
 #pragma unroll
@@ -907,6 +916,7 @@ __device__ __forceinline__ void merge_warps(WarpRows<D, RK, H16, H8>& st, float*
     }
   }
   q_sync();
+  // warp x of row block b is warp x * NRB + b
   float fo[NR], fz[NR];
 #pragma unroll
   for (int i = 0; i < NR; ++i) {
@@ -915,8 +925,7 @@ __device__ __forceinline__ void merge_warps(WarpRows<D, RK, H16, H8>& st, float*
     for (int x = 0; x < PEERS; ++x) M = fmaxf(M, ml[(x * NRB + rb) * 2 * RPW + row[i]]);
     fz[i] = st.m[i] == kNegInf ? 0.f : fast_exp2(st.m[i] - M);
     // O stands for weights 2^(w - m) times larger; in two factors, since w - m can pass 127
-    const float h = st.m[i] == kNegInf || st.w[i] == kNegInf ? kNegInf : 0.5f * (st.w[i] - M);
-    fo[i] = fast_exp2(h);
+    fo[i] = st.m[i] == kNegInf || st.w[i] == kNegInf ? 0.f : fast_exp2(0.5f * (st.w[i] - M));
   }
   if (tid < RP) {
     const int b = tid / RPW, r = tid % RPW;
@@ -931,61 +940,60 @@ __device__ __forceinline__ void merge_warps(WarpRows<D, RK, H16, H8>& st, float*
     rec[tid] = M;
     rec[RP + tid] = L;
   }
-  float* mine = mb + (peer * NRB + rb) * RPW * LD;
-  float* mO = rec + 2 * RP;
-  float* mZ = mO + RP * D;
-  auto reduce = [&](float* dst, int ld, int width) {  // dst[row][0 .. width) = sum over the peers
+  float zf[WR::OCT][2];  // fz of rows 2 t4, 2 t4 + 1 of each eight
+#pragma unroll
+  for (int x = 0; x < WR::OCT; ++x)
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      zf[x][e] = x < 2 * H16 ? __shfl_sync(0xFFFFFFFFu, fz[x], 8 * t4 + 4 * e) : fz[NR - 2 + e];
+#pragma unroll
+  for (int f0 = 0; f0 < NF; f0 += kQMergeFrags) {
+#pragma unroll
+    for (int f = f0; f < f0 + kQMergeFrags && f < NF; ++f) {
+      float4 v;
+      if (f < N16) {
+        const float* o = st.o16[H16 ? f : 0];
+        v = make_float4(o[0] * fo[0] * fo[0], o[1] * fo[0] * fo[0], o[2] * fo[1] * fo[1], o[3] * fo[1] * fo[1]);
+      } else if (f < N16 + N8) {
+        const float* o = st.o8[H8 ? f - N16 : 0];
+        const float a = fo[NR - 2], b = fo[NR - 1];
+        v = make_float4(o[0] * a * a, o[1] * b * b, o[2] * a * a, o[3] * b * b);
+      } else {
+        const int x = (f - N16 - N8) / MZ;
+        const float* z = st.z[x][(f - N16 - N8) % MZ];
+        v = make_float4(z[0] * zf[x][0], z[1] * zf[x][1], z[2] * zf[x][0], z[3] * zf[x][1]);
+      }
+      mb[(warp * kQMergeFrags + f - f0) * 32 + lane] = v;
+    }
     q_sync();
-    for (int e = 2 * tid; e < RP * width; e += 2 * kQThreads) {
-      const int r = e / width, col = e - r * width;
-      const float* src = mb + ((r / RPW) * RPW + r % RPW) * LD + col;
+    // a thread sums half a fragment's float4 of one row block over its warps
+    for (int e = tid; e < NRB * kQMergeFrags * 64; e += kQThreads) {
+      const int h = e & 1, ln = e >> 1 & 31, f = f0 + (e >> 6) % kQMergeFrags, b = (e >> 6) / kQMergeFrags;
+      if (f >= NF) continue;
+      const float2* src = reinterpret_cast<const float2*>(mb + (b * kQMergeFrags + f - f0) * 32 + ln) + h;
       float2 a = make_float2(0.f, 0.f);
 #pragma unroll
       for (int x = 0; x < PEERS; ++x) {
-        const float2 v = *reinterpret_cast<const float2*>(src + x * NRB * RPW * LD);
+        const float2 v = src[x * NRB * kQMergeFrags * 64];
         a.x += v.x;
         a.y += v.y;
       }
-      *reinterpret_cast<float2*>(dst + r * ld + col) = a;
+      const int g = ln >> 2, t = ln & 3;
+      if (f < N16) {  // rows g (+ 8), columns 8 f + 2 t, + 1
+        *reinterpret_cast<float2*>(rec + 2 * RP + (b * RPW + g + 8 * h) * D + 8 * f + 2 * t) = a;
+      } else {        // rows 2 t, 2 t + 1 of an octet, one column
+        const bool z = f >= N16 + N8;
+        const int x = z ? f - N16 - N8 : f - N16;
+        const int r = b * RPW + (z ? 8 * (x / MZ) : 16 * H16) + 2 * t, col = 16 * (z ? x % MZ : x) + 8 * h + g;
+        float* dst = rec + 2 * RP + (z ? RP * D + r * RK : r * D) + col;
+        if (!z || col < RK) {
+          dst[0] = a.x;
+          dst[z ? RK : D] = a.y;
+        }
+      }
     }
     q_sync();
-  };
-#pragma unroll
-  for (int c0 = 0; c0 < D; c0 += CW) {
-    if constexpr (H16) {
-#pragma unroll
-      for (int x = 0; x < CW / 8; ++x)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float* o = st.o16[c0 / 8 + x];
-          *reinterpret_cast<float2*>(mine + row[i] * LD + 8 * x + 2 * t4) =
-              make_float2(o[2 * i] * fo[i] * fo[i], o[2 * i + 1] * fo[i] * fo[i]);
-        }
-    }
-    if constexpr (H8) {
-#pragma unroll
-      for (int x = 0; x < CW / 16; ++x)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = R8 + (e & 1);
-          mine[row[i] * LD + 16 * x + 8 * (e >> 1) + g8] = st.o8[c0 / 16 + x][e] * fo[i] * fo[i];
-        }
-    }
-    reduce(mO + c0, D, CW);
   }
-#pragma unroll
-  for (int x = 0; x < WR::OCT; ++x) {
-    // fz of rows 2 t4, 2 t4 + 1 of these eight
-    const float f0 = x < 2 * H16 ? __shfl_sync(0xFFFFFFFFu, fz[x], 8 * t4) : fz[NR - 2];
-    const float f1 = x < 2 * H16 ? __shfl_sync(0xFFFFFFFFu, fz[x], 8 * t4 + 4) : fz[NR - 1];
-#pragma unroll
-    for (int mz = 0; mz < WR::MZ; ++mz)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (16 * mz + 8 * (e >> 1) < RK)
-          mine[(8 * x + 2 * t4 + (e & 1)) * LD + 16 * mz + 8 * (e >> 1) + g8] = st.z[x][mz][e] * (e & 1 ? f1 : f0);
-  }
-  reduce(mZ, RK, RK);
 }
 
 // Publish the record, or, as the last of the item's CTAs to get here (ticket),
@@ -996,10 +1004,20 @@ __device__ __forceinline__ void finish_item(const QDecodeParams& p, const Range&
   constexpr int REC = RP * (D + RK + 2);
   constexpr int E4 = RP * (D + RK) / 4;
   constexpr int PER = (E4 + kQThreads - 1) / kQThreads;
-  constexpr int TABLE = kQWarps * (RP > 16 && RP != 24 ? 16 : RP) * kQMergeLd;  // floats of the merge buffer
-  constexpr int CHUNK = TABLE / RP / 2;                                           // records whose m and l it holds
+  constexpr int CHUNK = kQWarps * kQMergeFrags * 128 / RP / 2;  // records whose m and l the merge buffer holds
   const int tid = threadIdx.x;
   const bool shared = !range.whole && (sg.lo > 0 || sg.hi < sg.nt);
+  // the B columns of the (agent, dim pair) units that this thread will write
+  constexpr int D2 = D / 2;
+  const int HD = p.Hkv * D, units = sg.n_ag * D2;
+  auto b_at = [&](int u) {
+    return reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.b) +
+                                             (size_t)(sg.i_lo + u / D2) * RK * HD + (size_t)sg.g * D + 2 * (u % D2));
+  };
+  if (tid < units) {  // into L1, while the record is published and merged
+#pragma unroll
+    for (int r = 0; r < RK; ++r) asm volatile("prefetch.global.L1 [%0];" ::"l"(b_at(tid) + (size_t)r * (HD / 2)));
+  }
   if (shared) {
     const int C = range.ctas, W = range.W;
     const int c_first = (int)owner_cta(sg.item_t0, W, C), c_last = (int)owner_cta(sg.item_t0 + sg.nt - 1, W, C);
@@ -1031,6 +1049,17 @@ __device__ __forceinline__ void finish_item(const QDecodeParams& p, const Range&
       rec[tid] = kNegInf;
       rec[RP + tid] = 0.f;
     }
+    constexpr int BATCH = 4;  // records whose loads are in flight together
+    float4 v[BATCH][PER];
+    auto fetch = [&](int j) {  // records j .. of the item (clamped)
+#pragma unroll
+      for (int q = 0; q < BATCH; ++q) {
+        const float4* src = reinterpret_cast<const float4*>(record(min(j + q, segs - 1)) + 2 * RP);
+#pragma unroll
+        for (int u = 0; u < PER; ++u)
+          if (tid + u * kQThreads < E4) v[q][u] = __ldcg(src + tid + u * kQThreads);
+      }
+    };
     for (int j0 = 0; j0 < segs; j0 += CHUNK) {
       const int nj = min(CHUNK, segs - j0);
       q_sync();
@@ -1043,7 +1072,9 @@ __device__ __forceinline__ void finish_item(const QDecodeParams& p, const Range&
       if (tid < RP) {
         const float before = rec[tid];
         float M = before, L = 0.f;
+#pragma unroll 4
         for (int j = 0; j < nj; ++j) M = fmaxf(M, t_m[j * RP + tid]);
+#pragma unroll 4
         for (int j = 0; j < nj; ++j) {
           const float mj = t_m[j * RP + tid];
           const float sc = mj == kNegInf ? 0.f : fast_exp2(mj - M);
@@ -1068,17 +1099,10 @@ __device__ __forceinline__ void finish_item(const QDecodeParams& p, const Range&
           acc[u].w *= c;
         }
       }
-      for (int jb = 0; jb < nj; jb += kMergeBatch) {
-        float4 v[kMergeBatch][PER];
+      for (int jb = 0; jb < nj; jb += BATCH) {
+        fetch(j0 + jb);
 #pragma unroll
-        for (int q = 0; q < kMergeBatch; ++q) {
-          const float4* src = reinterpret_cast<const float4*>(record(j0 + min(jb + q, nj - 1)) + 2 * RP);
-#pragma unroll
-          for (int u = 0; u < PER; ++u)
-            if (tid + u * kQThreads < E4) v[q][u] = __ldcg(src + tid + u * kQThreads);
-        }
-#pragma unroll
-        for (int q = 0; q < kMergeBatch; ++q) {
+        for (int q = 0; q < BATCH; ++q) {
           if (jb + q >= nj) break;
 #pragma unroll
           for (int u = 0; u < PER; ++u) {
@@ -1105,12 +1129,9 @@ __device__ __forceinline__ void finish_item(const QDecodeParams& p, const Range&
   const float* mL = rec + RP;
   const float* mO = rec + 2 * RP;
   const float* mZ = mO + RP * D;
-  constexpr int D2 = D / 2;
-  const int HD = p.Hkv * D;
-  for (int u = tid; u < sg.n_ag * D2; u += kQThreads) {
+  for (int u = tid; u < units; u += kQThreads) {
     const int agent = sg.i_lo + u / D2, dim = 2 * (u % D2);
-    const uint32_t* bp = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.b) +
-                                                           (size_t)agent * RK * HD + (size_t)sg.g * D + dim);
+    const uint32_t* bp = b_at(u);
     uint32_t b[RK];
 #pragma unroll
     for (int r = 0; r < RK; ++r) b[r] = __ldg(bp + (size_t)r * (HD / 2));
@@ -1140,10 +1161,10 @@ __device__ __forceinline__ void finish_item(const QDecodeParams& p, const Range&
   }
 }
 
-// Wait until a U stage holds U tile number un, then for its bytes.
-__device__ __forceinline__ bool q_wait_u(const QDecodeParams& p, const QBars& bar, int us, int un, uint32_t phase) {
+// Wait until a U stage that groups share holds tile number n's.
+__device__ __forceinline__ bool q_wait_turn(const QDecodeParams& p, const QBars& bar, int us, int n) {
   uint32_t spins = 0;
-  while (bar.useq[us] != un) {
+  while (bar.useq[us] != n) {
     if (*bar.abort_flag) return false;
     if (++spins >= p.spin_cap) {
       *bar.abort_flag = 1;
@@ -1151,7 +1172,7 @@ __device__ __forceinline__ bool q_wait_u(const QDecodeParams& p, const QBars& ba
       return false;
     }
   }
-  return q_wait(p, bar, &bar.u_full[us], phase);
+  return true;
 }
 
 template <int FMT, int D, int RK, int H16, int H8, int NRB>
@@ -1166,7 +1187,7 @@ __device__ void q_consumers(const QDecodeParams& p, uint8_t* smem, const QDecode
   const int rb = warp % NRB, peer = warp / NRB;  // row block; place among the warps that hold its rows
   const int og = peer / KW, kw = (peer % KW) * kQWarpKeys;
   float* rec = reinterpret_cast<float*>(smem + lay.rec_off);
-  float* mb = reinterpret_cast<float*>(smem + lay.mb_off);
+  float4* mb = reinterpret_cast<float4*>(smem + lay.mb_off);
   float* ml = reinterpret_cast<float*>(smem + lay.ml_off);
   uint32_t* qs = reinterpret_cast<uint32_t*>(smem + lay.q_off);
   int* a_sm = reinterpret_cast<int*>(smem + lay.a_off);
@@ -1220,7 +1241,7 @@ __device__ void q_consumers(const QDecodeParams& p, uint8_t* smem, const QDecode
         break;
       }
       const Entry* e = &bar.table[slot * kPlan + n % kPlan];
-      const int key0 = e->key0, u = e->u, un = e->un;
+      const int key0 = e->key0, u = e->u;
       const float ks = e->ks, vs = e->vs;
       if (__any_sync(0xFFFFFFFFu, !q_wait(p, bar, &bar.full[stage], phase))) {
         alive = false;
@@ -1236,7 +1257,9 @@ __device__ void q_consumers(const QDecodeParams& p, uint8_t* smem, const QDecode
       }
       if (u) {
         const int us = u >> 16 & 0xFF;
-        if (__any_sync(0xFFFFFFFFu, !q_wait_u(p, bar, us, un, u >> 24))) {
+        bool there = p.u_stages >= NG || q_wait_turn(p, bar, us, n);
+        there = there && q_wait(p, bar, &bar.u_full[us], u >> 24);
+        if (__any_sync(0xFFFFFFFFu, !there)) {
           alive = false;
           break;
         }
@@ -1261,7 +1284,7 @@ __device__ void q_consumers(const QDecodeParams& p, uint8_t* smem, const QDecode
       }
     }
     merge_warps<D, RK, H16, H8, NRB>(st, rec, mb, ml, rb, peer);
-    finish_item<D, RK, RP>(p, range, sg, rec, mb, bcast);
+    finish_item<D, RK, RP>(p, range, sg, rec, reinterpret_cast<float*>(mb), bcast);
     q_sync();  // the record, the merge buffer and the offsets are free again
   }
 }
@@ -1326,7 +1349,7 @@ __global__ void __launch_bounds__(kQBlockThreads, 1)
     setmaxnreg_dec<kQProducerRegs>();
     // the test hook (p.stall): nothing is copied, so the consumers' waits run out
     if (warp == kQWarps + 2) {
-      q_plan(p, bar, r);
+      q_plan<kQWarps / (kQBlock / kQWarpKeys) / NRB>(p, bar, r);
     } else if (warp == kQWarps && !p.stall) {
       if ((threadIdx.x & 31) == 0) q_produce_kv<D>(p, &tmK, &tmV, smem, lay, bar);
     } else if (warp == kQWarps + 1 && !p.stall) {

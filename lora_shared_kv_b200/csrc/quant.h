@@ -92,9 +92,8 @@ __host__ __device__ constexpr QShape q_shape(int rows) {
 
 __host__ __device__ constexpr int q_groups(int nrb) { return kQWarps / (kQBlock / kQWarpKeys) / nrb; }
 
-// Columns of O that the warps exchange per pass when their rows are merged.
-constexpr int kQMergeCols = 32;
-constexpr int kQMergeLd = kQMergeCols + 8;  // row stride: four rows' float2 writes lie in different banks
+// Accumulator fragments that the warps exchange per pass when their rows are merged.
+constexpr int kQMergeFrags = 4;
 constexpr int kQPlanBytes = 4 * 32 * 32, kQPlanBarriers = 12;  // the planner's table of tiles
 
 // Shared-memory plan (bytes from a 1024-aligned base).
@@ -110,8 +109,8 @@ __host__ __device__ inline QDecodeSmem q_smem_plan(int D, int RK, int rows_block
   s.u_bytes = n_u_slots * kQBlock * RK * 2;
   s.u_off = stages * s.tile_bytes;
   s.rec_off = s.u_off + u_stages * s.u_bytes;                            // [m | l | O | Z] of RP rows
-  s.mb_off = s.rec_off + RP * (D + RK + 2) * 4;                          // the warps' columns being merged
-  s.ml_off = s.mb_off + kQWarps * rows_block * kQMergeLd * 4;            // the warps' m and l
+  s.mb_off = round_up(s.rec_off + RP * (D + RK + 2) * 4, 16);                        // the warps' fragments being merged
+  s.ml_off = s.mb_off + kQWarps * kQMergeFrags * 512;                    // the warps' m and l
   s.q_off = round_up(s.ml_off + kQWarps * rows_block * 2 * 4, 16);       // 24-row blocks: query fragments
   s.plan_off = s.q_off + (rows_block == 24 ? 24 * D * 2 : 0);            // the planner's table
   s.a_off = s.plan_off + kQPlanBytes;                                    // offsets of the item's agents

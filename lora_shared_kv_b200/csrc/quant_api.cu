@@ -128,15 +128,16 @@ lrkv_status plan_decode_quant(const lrkv_problem* p, int max_seq_len, const Devi
   const lrkv::QShape sh = lrkv::q_shape(pl->rows_per_group);
   const int rows_block = 16 * sh.h16 + 8 * sh.h8;
   pl->RP = rows_block * sh.nrb;
-  // Up to four U stages within 80 KB (one per tile being worked on), then as many
-  // K/V stages as fit, up to 16, in multiples of the consumer groups.
+  // One U stage per consumer group (fewer where U tiles are large), as long as two K/V
+  // stages per group fit beside them; then as many K/V stages as fit, up to 16, in
+  // multiples of the groups.
   const int optin = dev.smem_optin > 0 ? dev.smem_optin : 232448;
-  const int u_bytes = pl->n_u_slots * LRKV_QUANT_BLOCK * p->rank * 2;
-  pl->u_stages = u_bytes > 81920 / 2 ? 1 : u_bytes * 4 > 81920 ? 81920 / u_bytes : 4;
+  const int groups = lrkv::q_groups(sh.nrb);
   auto smem_of = [&](int stages) {
     return lrkv::q_smem_plan(p->head_dim, p->rank, rows_block, sh.nrb, pl->n_u_slots, stages, pl->u_stages).total + 1024;
   };
-  const int groups = lrkv::q_groups(sh.nrb);
+  pl->u_stages = groups;
+  while (pl->u_stages > 1 && smem_of(2 * groups) > optin) --pl->u_stages;
   int stages = 16;
   while (stages >= groups && smem_of(stages) > optin) stages -= groups;
   if (stages < groups) return fail(LRKV_ERR_UNSUPPORTED, "decode tiles do not fit in shared memory");
