@@ -288,10 +288,10 @@ def kv_view_quant_paged(k8_pages, v8_pages, k_scale, v_scale, page_table):
 
 def _quant_fits(view, problem, rows):
     """The view's buffers hold the problem's sessions, KV heads and head_dim, and `rows` rows of each."""
-    need = (problem.num_sessions, problem.num_kv_heads, int(rows), problem.head_dim)
-    _require(all(h >= n for h, n in zip(view.holds, need)) and view.holds[3] == need[3],
-             f"the 8-bit view holds [sessions, KV heads, rows, head_dim] {view.holds}, the call needs {need}")
-    _on_device(**{f"8-bit view tensor {i}": t for i, t in enumerate(view.tensors)})
+    S, H, L, d = view.holds
+    if S < problem.num_sessions or H < problem.num_kv_heads or L < rows or d != problem.head_dim:
+        need = (problem.num_sessions, problem.num_kv_heads, int(rows), problem.head_dim)
+        raise ValueError(f"the 8-bit view holds [sessions, KV heads, rows, head_dim] {view.holds}, the call needs {need}")
 
 
 def u_view(u):
@@ -416,33 +416,54 @@ def lrkv_attn_prefill_chunk(problem, q, kv, session, ctx_len, T, u, b, offsets, 
                                          _ptr(out), odt, _ptr(workspace), nbytes, _stream(stream)))
 
 
-def _row_ranges(problem, first_rows, row_counts, workspace):
+def _on_current(*tensors):
+    """_on_device for the calls whose launch costs count: one comparison a tensor (a host tensor's device is -1),
+    the full check for its error only where one differs.  Returns the device."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            _on_device(**{f"tensor {i}": x for i, x in enumerate(tensors)})
+    return dev
+
+
+def _raw_stream(stream, dev):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _rows_of(problem, first_rows, row_counts):
     for name, t in (("first_rows", first_rows), ("row_counts", row_counts)):
         if t is not None:
             _require(t.dtype == torch.int32 and t.is_contiguous() and t.numel() >= problem.num_sessions,
                      f"{name}: int32 [num_sessions], contiguous")
-    _on_device(first_rows=first_rows, row_counts=row_counts, workspace=workspace)
 
 
 def lrkv_quantize_kv(problem, src, T, dst, dst_rows, first_rows, row_counts, workspace, stream=None):
     """Write rows [0, n) of every session of the bf16 view `src` into rows [f, f + n) of the 8-bit view `dst`, which
     holds dst_rows rows a session: f = first_rows[s] (0 when None), n = row_counts[s] (T when None).  The cache then
     holds f + n tokens of the session."""
-    _row_ranges(problem, first_rows, row_counts, workspace)
+    _rows_of(problem, first_rows, row_counts)
     _quant_fits(dst, problem, dst_rows)
-    _check(lib().lrkv_quantize_kv(ctypes.byref(problem), ctypes.byref(src), int(T), ctypes.byref(dst), int(dst_rows),
-                                  _ptr(first_rows), _ptr(row_counts), _ptr(workspace),
-                                  workspace.numel() * workspace.element_size(), _stream(stream)))
+    dev = _on_current(first_rows, row_counts, workspace, *dst.tensors)
+    _check(lib().lrkv_quantize_kv(problem, src, T, dst, dst_rows, _at(first_rows), _at(row_counts),
+                                  workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                  _raw_stream(stream, dev)))
 
 
 def lrkv_dequantize_kv(problem, src, src_rows, T, dst, first_rows, row_counts, workspace, stream=None):
     """Read rows [f, f + n) of every session of the 8-bit view `src` (src_rows rows a session) back into rows [0, n)
     of the bf16 view `dst`; f, n and T as in lrkv_quantize_kv."""
-    _row_ranges(problem, first_rows, row_counts, workspace)
+    _rows_of(problem, first_rows, row_counts)
     _quant_fits(src, problem, src_rows)
-    _check(lib().lrkv_dequantize_kv(ctypes.byref(problem), ctypes.byref(src), int(src_rows), int(T),
-                                    ctypes.byref(dst), _ptr(first_rows), _ptr(row_counts), _ptr(workspace),
-                                    workspace.numel() * workspace.element_size(), _stream(stream)))
+    dev = _on_current(first_rows, row_counts, workspace, *src.tensors)
+    _check(lib().lrkv_dequantize_kv(problem, src, src_rows, T, dst, _at(first_rows), _at(row_counts),
+                                    workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                    _raw_stream(stream, dev)))
 
 
 def lrkv_decode_quant_workspace_bytes(problem, max_seq_len):
@@ -454,26 +475,26 @@ def lrkv_decode_quant_workspace_bytes(problem, max_seq_len):
 
 def lrkv_attn_decode_quant(problem, q, kv, seq_lens, max_seq_len, u, b, offsets, out, workspace, stream=None):
     """lrkv_attn_decode over an 8-bit base cache (kv: a kv_view_quant_dense or kv_view_quant_paged view)."""
+    p = problem
     _require(q.is_contiguous() and b.is_contiguous() and out.is_contiguous(), "q, b and out must be contiguous")
     _require(q.dtype == torch.bfloat16 and b.dtype == torch.bfloat16, "q and b: bf16")
-    _require(out.dtype in (torch.bfloat16, torch.float32), "out: bf16 or fp32")
-    _require(seq_lens.dtype == torch.int32 and seq_lens.is_contiguous() and seq_lens.numel() >= problem.num_sessions,
+    odt = F32 if out.dtype == torch.float32 else BF16
+    _require(odt == F32 or out.dtype == torch.bfloat16, "out: bf16 or fp32")
+    _require(seq_lens.dtype == torch.int32 and seq_lens.is_contiguous() and seq_lens.numel() >= p.num_sessions,
              "seq_lens: int32 [num_sessions], contiguous")
-    rows = problem.num_sessions * problem.num_agents
+    rows = p.num_sessions * p.num_agents
     _require(offsets is None or (offsets.dtype == torch.int32 and offsets.is_contiguous() and offsets.numel() >= rows),
              "offsets: int32 [num_sessions, num_agents], contiguous, or None")
-    size = rows * problem.num_q_heads * problem.head_dim
+    size = rows * p.num_q_heads * p.head_dim
     _require(q.numel() >= size and out.numel() >= size, "q and out: [num_sessions, num_agents, num_q_heads, head_dim]")
-    _require(b.numel() >= problem.num_agents * problem.rank * problem.num_kv_heads * problem.head_dim,
+    _require(b.numel() >= p.num_agents * p.rank * p.num_kv_heads * p.head_dim,
              "b: [num_agents, rank, num_kv_heads * head_dim]")
-    _on_device(q=q, seq_lens=seq_lens, b=b, offsets=offsets, out=out, workspace=workspace)
-    _quant_fits(kv, problem, max_seq_len)
-    odt = F32 if out.dtype == torch.float32 else BF16
+    _quant_fits(kv, p, max_seq_len)
+    dev = _on_current(q, seq_lens, b, offsets, out, workspace, *kv.tensors)
     uv = u if isinstance(u, UView) else u_view(u)
-    _check(lib().lrkv_attn_decode_quant(ctypes.byref(problem), _ptr(q), ctypes.byref(kv), _ptr(seq_lens),
-                                        int(max_seq_len), ctypes.byref(uv), _ptr(b), _ptr(offsets), _ptr(out), odt,
-                                        _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                        _stream(stream)))
+    _check(lib().lrkv_attn_decode_quant(p, q.data_ptr(), kv, seq_lens.data_ptr(), max_seq_len, uv, b.data_ptr(),
+                                        _at(offsets), out.data_ptr(), odt, workspace.data_ptr(),
+                                        workspace.numel() * workspace.element_size(), _raw_stream(stream, dev)))
 
 
 def lrkv_workspace_reset(workspace, stream=None):

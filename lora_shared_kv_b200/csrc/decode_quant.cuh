@@ -55,7 +55,7 @@ struct Range {
   int W, ctas;          // tiles of the launch; CTAs that take part
   int t_begin, t_end;   // this CTA's tiles
   int s, base, sl;      // session of t_begin, its first tile, its length
-  int whole;            // whole items, one per CTA
+  int per_item;         // CTAs of every item (aligned shares), or 0
 };
 
 // First tile of CTA c when W tiles are split evenly: floor(c W / C), in 32 bits.
@@ -110,12 +110,13 @@ __device__ __forceinline__ void find_range(const QDecodeParams& p, Range* out) {
   const int C = W < (int)gridDim.x ? W : (int)gridDim.x;
   Range r = {};
   r.W = W;
-  r.whole = q_whole_items(items, C, nt_max, W, p.whole_slack);
-  r.ctas = r.whole ? items : C;
+  r.per_item = q_item_ctas(items, C, nt_max, W, p.slack);
+  r.ctas = r.per_item ? items * r.per_item : C;
   if (c < r.ctas) {
-    r.t_begin = r.whole ? 0 : range_begin(c, W, C);
-    r.t_end = r.whole ? 0 : range_begin(c + 1, W, C);
-    const int s_whole = c / HR;
+    const int item = r.per_item ? c / r.per_item : 0;
+    r.t_begin = r.per_item ? 0 : range_begin(c, W, C);
+    r.t_end = r.per_item ? 0 : range_begin(c + 1, W, C);
+    const int s_item = item / HR;
     // the session that holds the first tile (or item), and its first tile
     for (int s0 = 0, base = 0; s0 < p.S; s0 += 32) {
       const int s = s0 + lane;
@@ -128,16 +129,20 @@ __device__ __forceinline__ void find_range(const QDecodeParams& p, Range* out) {
         if (lane >= o) incl += up;
       }
       const int mine = base + (incl - nt) * HR;
-      const bool here = s < p.S && (r.whole ? s == s_whole : (r.t_begin >= mine && r.t_begin < mine + nt * HR));
+      const bool here = s < p.S && (r.per_item ? s == s_item : (r.t_begin >= mine && r.t_begin < mine + nt * HR));
       const unsigned hit = __ballot_sync(0xFFFFFFFFu, here);
       if (hit) {
         const int src = __ffs(hit) - 1;
         r.s = s0 + src;
         r.base = __shfl_sync(0xFFFFFFFFu, mine, src);
         r.sl = __shfl_sync(0xFFFFFFFFu, sl, src);
-        if (r.whole) {
-          r.t_begin = r.base + (c - s_whole * HR) * tiles_of(r.sl);
-          r.t_end = r.t_begin + tiles_of(r.sl);
+        if (r.per_item) {  // this CTA's even part of its item
+          const int tiles = tiles_of(r.sl), t0 = r.base + (item - s_item * HR) * tiles, k = c - item * r.per_item;
+          const int parts = min(r.per_item, tiles);  // the last CTAs of a short item have none
+          if (k < parts) {
+            r.t_begin = t0 + range_begin(k, tiles, parts);
+            r.t_end = t0 + range_begin(k + 1, tiles, parts);
+          }
         }
         break;
       }
@@ -307,7 +312,7 @@ __device__ __forceinline__ void q_plan(const QDecodeParams& p, const QBars& bar,
     const int my_a = lane < sg.n_ag ? load_offset(p, sg.s, sg.i_lo + lane, false) : 0x7fffffff;
     const int32_t* pages = p.page_table + (size_t)sg.s * p.pt_stride;
     QOrder ord;
-    ord.start(sg.nt, p.balance && !range.whole);
+    ord.start(sg.nt, p.balance && range.per_item != 1);
     for (int k = 0; k < tiles;) {
       if (!open()) return;
       const int slot = n % kPlan, m = min(kPlan - slot, tiles - k);  // this pass: m tiles
@@ -996,17 +1001,19 @@ __device__ __forceinline__ void merge_warps(WarpRows<D, RK, H16, H8>& st, float*
   }
 }
 
-// Publish the record, or, as the last of the item's CTAs to get here (ticket),
-// combine every record of the item; then out = (O + Z B_i,g) / l.
+// Publish the record, or, as the last of the item's CTAs to get here (ticket), combine
+// every record of the item; then out = (O + Z B_i,g) / l.  `table` holds kQMaxCtas x RP
+// floats.
 template <int D, int RK, int RP>
 __device__ __forceinline__ void finish_item(const QDecodeParams& p, const Range& range, const Seg& sg, float* rec,
                                             float* table, int* bcast) {
+  constexpr int THREADS = kQThreads;
+  const int tid = threadIdx.x;
   constexpr int REC = RP * (D + RK + 2);
   constexpr int E4 = RP * (D + RK) / 4;
-  constexpr int PER = (E4 + kQThreads - 1) / kQThreads;
-  constexpr int CHUNK = kQWarps * kQMergeFrags * 128 / RP / 2;  // records whose m and l the merge buffer holds
-  const int tid = threadIdx.x;
-  const bool shared = !range.whole && (sg.lo > 0 || sg.hi < sg.nt);
+  constexpr int PER = (E4 + THREADS - 1) / THREADS;  // float4 elements of a thread
+  constexpr int BATCH = 4;                            // records whose loads are in flight together
+  const bool shared = sg.lo > 0 || sg.hi < sg.nt;
   // the B columns of the (agent, dim pair) units that this thread will write
   constexpr int D2 = D / 2;
   const int HD = p.Hkv * D, units = sg.n_ag * D2;
@@ -1019,11 +1026,18 @@ __device__ __forceinline__ void finish_item(const QDecodeParams& p, const Range&
     for (int r = 0; r < RK; ++r) asm volatile("prefetch.global.L1 [%0];" ::"l"(b_at(tid) + (size_t)r * (HD / 2)));
   }
   if (shared) {
+    // the CTAs that hold a part of the item
     const int C = range.ctas, W = range.W;
-    const int c_first = (int)owner_cta(sg.item_t0, W, C), c_last = (int)owner_cta(sg.item_t0 + sg.nt - 1, W, C);
-    const int segs = c_last - c_first + 1;
+    int c_first, segs;
+    if (range.per_item) {
+      c_first = sg.item * range.per_item;
+      segs = min(range.per_item, sg.nt);
+    } else {
+      c_first = (int)owner_cta(sg.item_t0, W, C);
+      segs = (int)owner_cta(sg.item_t0 + sg.nt - 1, W, C) - c_first + 1;
+    }
     float* mine = p.partials + q_record_slot(blockIdx.x, range.t_begin, sg.item_t0) * REC;
-    for (int e = 4 * tid; e < REC; e += 4 * kQThreads)
+    for (int e = 4 * tid; e < REC; e += 4 * THREADS)
       __stcg(reinterpret_cast<float4*>(mine + e), *reinterpret_cast<const float4*>(rec + e));
     q_sync();
     if (tid == 0) {
@@ -1036,79 +1050,47 @@ __device__ __forceinline__ void finish_item(const QDecodeParams& p, const Range&
     if (!*bcast) return;
     __threadfence();
     // Only the item's first CTA can hold it in its second record slot.
-    const float* first = p.partials + q_record_slot(c_first, range_begin(c_first, W, C), sg.item_t0) * REC;
+    const float* first =
+        p.partials + q_record_slot(c_first, range.per_item ? sg.item_t0 : range_begin(c_first, W, C), sg.item_t0) * REC;
     const float* rest = p.partials + 2 * (size_t)c_first * REC;
     auto record = [&](int j) { return j == 0 ? first : rest + (size_t)(2 * j) * REC; };
-    float4 acc[PER];
-#pragma unroll
-    for (int u = 0; u < PER; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-    float* t_m = table;                // [CHUNK][RP]: the records' m, then their scales
-    float* t_l = table + CHUNK * RP;   // their l
-    float* corr = rec + 2 * RP;        // what a new maximum does to the sums so far (O's place: free until the end)
-    if (tid < RP) {
-      rec[tid] = kNegInf;
-      rec[RP + tid] = 0.f;
+    for (int e = tid; e < segs * RP; e += THREADS) table[e] = __ldcg(record(e / RP) + e % RP);  // the records' m
+    q_sync();
+    if (tid < RP) {  // RP <= 32 <= THREADS
+      float M = kNegInf, L = 0.f;
+#pragma unroll 4
+      for (int j = 0; j < segs; ++j) M = fmaxf(M, table[j * RP + tid]);
+#pragma unroll 4
+      for (int j = 0; j < segs; ++j) {
+        const float mj = table[j * RP + tid], lj = __ldcg(record(j) + RP + tid);
+        const float sc = mj == kNegInf ? 0.f : fast_exp2(mj - M);
+        table[j * RP + tid] = sc;
+        L += sc == 0.f ? 0.f : lj * sc;
+      }
+      rec[RP + tid] = L;
     }
-    constexpr int BATCH = 4;  // records whose loads are in flight together
-    float4 v[BATCH][PER];
-    auto fetch = [&](int j) {  // records j .. of the item (clamped)
+    q_sync();
+    {  // O and Z
+      float4 acc[PER];
 #pragma unroll
-      for (int q = 0; q < BATCH; ++q) {
-        const float4* src = reinterpret_cast<const float4*>(record(min(j + q, segs - 1)) + 2 * RP);
-#pragma unroll
-        for (int u = 0; u < PER; ++u)
-          if (tid + u * kQThreads < E4) v[q][u] = __ldcg(src + tid + u * kQThreads);
-      }
-    };
-    for (int j0 = 0; j0 < segs; j0 += CHUNK) {
-      const int nj = min(CHUNK, segs - j0);
-      q_sync();
-      for (int e = tid; e < nj * RP; e += kQThreads) {
-        const float* r = record(j0 + e / RP) + e % RP;
-        t_m[e] = __ldcg(r);
-        t_l[e] = __ldcg(r + RP);
-      }
-      q_sync();
-      if (tid < RP) {
-        const float before = rec[tid];
-        float M = before, L = 0.f;
-#pragma unroll 4
-        for (int j = 0; j < nj; ++j) M = fmaxf(M, t_m[j * RP + tid]);
-#pragma unroll 4
-        for (int j = 0; j < nj; ++j) {
-          const float mj = t_m[j * RP + tid];
-          const float sc = mj == kNegInf ? 0.f : fast_exp2(mj - M);
-          t_m[j * RP + tid] = sc;
-          L += sc == 0.f ? 0.f : t_l[j * RP + tid] * sc;
-        }
-        const float c = before == kNegInf ? 0.f : fast_exp2(before - M);
-        rec[tid] = M;
-        rec[RP + tid] = rec[RP + tid] * c + L;
-        corr[tid] = c;
-      }
-      q_sync();
-      if (j0 > 0) {
-#pragma unroll
-        for (int u = 0; u < PER; ++u) {
-          const int e = 4 * (tid + u * kQThreads);
-          if (e >= 4 * E4) continue;
-          const float c = corr[e < RP * D ? e / D : (e - RP * D) / RK];
-          acc[u].x *= c;
-          acc[u].y *= c;
-          acc[u].z *= c;
-          acc[u].w *= c;
-        }
-      }
-      for (int jb = 0; jb < nj; jb += BATCH) {
-        fetch(j0 + jb);
+      for (int u = 0; u < PER; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int jb = 0; jb < segs; jb += BATCH) {
+        float4 v[BATCH][PER];
 #pragma unroll
         for (int q = 0; q < BATCH; ++q) {
-          if (jb + q >= nj) break;
+          const float4* src = reinterpret_cast<const float4*>(record(min(jb + q, segs - 1)) + 2 * RP);
+#pragma unroll
+          for (int u = 0; u < PER; ++u)
+            if (tid + u * THREADS < E4) v[q][u] = __ldcg(src + tid + u * THREADS);
+        }
+#pragma unroll
+        for (int q = 0; q < BATCH; ++q) {
+          if (jb + q >= segs) break;
 #pragma unroll
           for (int u = 0; u < PER; ++u) {
-            const int e = 4 * (tid + u * kQThreads);
+            const int e = 4 * (tid + u * THREADS);
             if (e >= 4 * E4) continue;
-            const float sc = t_m[(jb + q) * RP + (e < RP * D ? e / D : (e - RP * D) / RK)];
+            const float sc = table[(jb + q) * RP + (e < RP * D ? e / D : (e - RP * D) / RK)];
             acc[u].x += v[q][u].x * sc;
             acc[u].y += v[q][u].y * sc;
             acc[u].z += v[q][u].z * sc;
@@ -1116,12 +1098,11 @@ __device__ __forceinline__ void finish_item(const QDecodeParams& p, const Range&
           }
         }
       }
-    }
-    q_sync();  // corr has been read
 #pragma unroll
-    for (int u = 0; u < PER; ++u) {
-      const int e4 = tid + u * kQThreads;
-      if (e4 < E4) *reinterpret_cast<float4*>(rec + 2 * RP + 4 * e4) = acc[u];
+      for (int u = 0; u < PER; ++u) {
+        const int e4 = tid + u * THREADS;
+        if (e4 < E4) *reinterpret_cast<float4*>(rec + 2 * RP + 4 * e4) = acc[u];
+      }
     }
     q_sync();
   }
@@ -1129,7 +1110,7 @@ __device__ __forceinline__ void finish_item(const QDecodeParams& p, const Range&
   const float* mL = rec + RP;
   const float* mO = rec + 2 * RP;
   const float* mZ = mO + RP * D;
-  for (int u = tid; u < units; u += kQThreads) {
+  for (int u = tid; u < units; u += THREADS) {
     const int agent = sg.i_lo + u / D2, dim = 2 * (u % D2);
     const uint32_t* bp = b_at(u);
     uint32_t b[RK];

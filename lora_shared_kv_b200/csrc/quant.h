@@ -66,7 +66,7 @@ struct QDecodeParams {
   int num_pages;
   int stages, u_stages;      // ring stages of K/V tiles and of U tiles
   int balance;               // visit an item's tiles in a low-discrepancy order (QOrder)
-  int whole_slack;           // see q_whole_items
+  int slack;                 // see q_item_ctas
   float scale_log2;          // softmax_scale * log2(e)
   float* partials;           // two records per CTA: see q_record_slot
   int* tickets;              // one per work item
@@ -94,6 +94,7 @@ __host__ __device__ constexpr int q_groups(int nrb) { return kQWarps / (kQBlock 
 
 // Accumulator fragments that the warps exchange per pass when their rows are merged.
 constexpr int kQMergeFrags = 4;
+constexpr int kQMaxCtas = 160;  // CTAs of a launch at most (and so partial records of an item)
 constexpr int kQPlanBytes = 4 * 32 * 32, kQPlanBarriers = 12;  // the planner's table of tiles
 
 // Shared-memory plan (bytes from a 1024-aligned base).
@@ -109,13 +110,14 @@ __host__ __device__ inline QDecodeSmem q_smem_plan(int D, int RK, int rows_block
   s.u_bytes = n_u_slots * kQBlock * RK * 2;
   s.u_off = stages * s.tile_bytes;
   s.rec_off = s.u_off + u_stages * s.u_bytes;                            // [m | l | O | Z] of RP rows
-  s.mb_off = round_up(s.rec_off + RP * (D + RK + 2) * 4, 16);                        // the warps' fragments being merged
-  s.ml_off = s.mb_off + kQWarps * kQMergeFrags * 512;                    // the warps' m and l
+  s.mb_off = round_up(s.rec_off + RP * (D + RK + 2) * 4, 16);                        // the warps' fragments, then the records' scales
+  const int mb_bytes = kQWarps * kQMergeFrags * 512, table_bytes = kQMaxCtas * RP * 4;
+  s.ml_off = s.mb_off + (mb_bytes > table_bytes ? mb_bytes : table_bytes);  // the warps' m and l
   s.q_off = round_up(s.ml_off + kQWarps * rows_block * 2 * 4, 16);       // 24-row blocks: query fragments
   s.plan_off = s.q_off + (rows_block == 24 ? 24 * D * 2 : 0);            // the planner's table
   s.a_off = s.plan_off + kQPlanBytes;                                    // offsets of the item's agents
   s.bar_off = round_up(s.a_off + kMaxAgents * 4, 16);
-  s.useq_off = s.bar_off + (2 * (stages + u_stages) + kQPlanBarriers) * 8;                 // tile number of each U stage
+  s.useq_off = s.bar_off + (2 * (stages + u_stages) + kQPlanBarriers) * 8;  // tile number of each U stage
   s.misc_off = round_up(s.useq_off + u_stages * 4, 16);                  // the CTA's range, abort word, broadcast word
   s.total = s.misc_off + 96;
   return s;
@@ -123,11 +125,16 @@ __host__ __device__ inline QDecodeSmem q_smem_plan(int D, int RK, int rows_block
 
 inline size_t q_record_floats(int RP, int D, int RK) { return (size_t)RP * (D + RK + 2); }
 
-// A CTA takes whole items, one each, when there are no more items than CTAs and
-// the longest item is at most `slack` tiles above the even share: nothing is
-// then published or merged.
-__host__ __device__ inline bool q_whole_items(int items, int ctas, int nt_max, int W, int slack) {
-  return items <= ctas && nt_max <= (W + ctas - 1) / ctas + slack;
+constexpr int kQSlackTiles = 16;
+
+// CTAs per item when every item takes the same number, or 0 for the even split of all
+// tiles.  Aligned shares end where items end: a CTA then finishes one stretch of one
+// item, where the even split's CTAs mostly finish two (and a CTA that holds a whole item
+// has nothing to publish or merge).  They are taken when the longest share is at most
+// `slack` tiles above the even one.
+__host__ __device__ inline int q_item_ctas(int items, int ctas, int nt_max, int W, int slack) {
+  const int k = items > 0 ? ctas / items : 0;
+  return k > 0 && (nt_max + k - 1) / k <= (W + ctas - 1) / ctas + slack ? k : 0;
 }
 
 lrkv_status launch_decode_quant(const QDecodeParams& p, int D, int RK, int rows, int fmt, const void* tmK,

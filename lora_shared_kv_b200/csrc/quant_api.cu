@@ -122,7 +122,7 @@ lrkv_status plan_decode_quant(const lrkv_problem* p, int max_seq_len, const Devi
   pl->items = p->num_sessions * per_session;
   if (pl->items > 0x3FFFFFFF || pl->items * pl->nt > 0x7FFF0000)
     return fail(LRKV_ERR_UNSUPPORTED, "too many (session, KV head, row group) items or tiles");
-  const int sms = dev.sms > 0 ? dev.sms : 148;
+  const int sms = dev.sms < 1 ? 148 : dev.sms > lrkv::kQMaxCtas ? lrkv::kQMaxCtas : dev.sms;
   const long long W = pl->items * pl->nt;
   pl->ctas = (int)(W < sms ? W : sms);
   const lrkv::QShape sh = lrkv::q_shape(pl->rows_per_group);
@@ -275,7 +275,7 @@ lrkv_status lrkv_attn_decode_quant(const lrkv_problem* p, const void* q, const l
   dp.stages = pl.stages;
   dp.u_stages = pl.u_stages;
   dp.balance = p->mode == LRKV_BASE_SHARED;
-  dp.whole_slack = lrkv::kWholeItemSlackTiles;
+  dp.slack = lrkv::kQSlackTiles;
   dp.scale_log2 = scale_of(p) * 1.4426950408889634f;
   char* ws = static_cast<char*>(workspace);
   dp.flags = reinterpret_cast<unsigned*>(ws);
