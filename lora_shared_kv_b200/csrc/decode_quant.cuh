@@ -30,9 +30,10 @@
 //    p' between 2^8 and 2^15 (fp16 ends at 2^16 and is full-precision down to
 //    2^-14).  So p' carries 11 bits down to 2^-22 of the largest weight and 2^-33
 //    absolute, whatever the scales.  The low-rank product takes p as bf16.
-//  * The flattened (item, tile) space of the actual lengths is split evenly over
-//    the CTAs (each counts the sessions' tiles at its start), so ragged batches
-//    are balanced; an item cut between CTAs is merged by the last one to finish.
+//  * The items' tiles of the actual lengths, and what an item costs beside them, are
+//    split evenly over the CTAs (each counts the sessions' tiles at its start), so
+//    ragged batches are balanced; an item cut between CTAs is merged by the last one
+//    to finish.
 //  * Keys past seq_len and U rows before a_i are removed by selects on operands.
 #pragma once
 
@@ -49,16 +50,16 @@ namespace {
 
 constexpr float kNegInf = -INFINITY;
 
-// The CTA's share of the work, found by warp 0.  Tiles of a launch are counted in 32
-// bits (checked on the host).
+// The CTA's share of the work, found by warp 0.  Units (an item's kQItemUnits, then its
+// tiles) are counted in 32 bits (checked on the host).
 struct Range {
-  int W, ctas;          // tiles of the launch; CTAs that take part
-  int t_begin, t_end;   // this CTA's tiles
-  int s, base, sl;      // session of t_begin, its first tile, its length
+  int W, ctas;          // units of the launch; CTAs that take part
+  int t_begin, t_end;   // this CTA's units
+  int s, base, sl;      // session of t_begin, its first unit, its length
   int per_item;         // CTAs of every item (aligned shares), or 0
 };
 
-// First tile of CTA c when W tiles are split evenly: floor(c W / C), in 32 bits.
+// First unit of CTA c when W units are split evenly: floor(c W / C), in 32 bits.
 __device__ __forceinline__ int range_begin(int c, int W, int C) {
   const int q = W / C;
   return c * q + c * (W - q * C) / C;
@@ -86,8 +87,9 @@ __device__ __forceinline__ int clamp_len(const QDecodeParams& p, int sl) {
 __device__ __forceinline__ int session_len(const QDecodeParams& p, int s) { return clamp_len(p, __ldg(p.seq_lens + s)); }
 // An empty session keeps one (empty) tile per item, so that its rows are written.
 __device__ __forceinline__ int tiles_of(int sl) { return sl > 0 ? (sl + kQBlock - 1) / kQBlock : 1; }
+__device__ __forceinline__ int units_of(int sl) { return tiles_of(sl) + kQItemUnits; }
 
-// Warp 0: count every session's tiles, then find this CTA's range.
+// Warp 0: count every session's units, then find this CTA's range.
 __device__ __forceinline__ void find_range(const QDecodeParams& p, Range* out) {
   const int lane = threadIdx.x & 31;
   const int HR = p.Hkv * p.n_rg;
@@ -99,7 +101,7 @@ __device__ __forceinline__ void find_range(const QDecodeParams& p, Range* out) {
       const int given = __ldg(p.seq_lens + s);
       sl = clamp_len(p, given);
       bad |= sl != given;
-      total += tiles_of(sl);
+      total += units_of(sl);
       nt_max = max(nt_max, tiles_of(sl));
     }
   }
@@ -110,26 +112,26 @@ __device__ __forceinline__ void find_range(const QDecodeParams& p, Range* out) {
   const int C = W < (int)gridDim.x ? W : (int)gridDim.x;
   Range r = {};
   r.W = W;
-  r.per_item = q_item_ctas(items, C, nt_max, W, p.slack);
+  r.per_item = q_item_ctas(items, C, nt_max, W);
   r.ctas = r.per_item ? items * r.per_item : C;
   if (c < r.ctas) {
     const int item = r.per_item ? c / r.per_item : 0;
     r.t_begin = r.per_item ? 0 : range_begin(c, W, C);
     r.t_end = r.per_item ? 0 : range_begin(c + 1, W, C);
     const int s_item = item / HR;
-    // the session that holds the first tile (or item), and its first tile
+    // the session that holds the first unit (or the item), and its first unit
     for (int s0 = 0, base = 0; s0 < p.S; s0 += 32) {
       const int s = s0 + lane;
       if (p.S > 32) sl = s < p.S ? session_len(p, s) : 0;  // else still held from above
-      const int nt = s < p.S ? tiles_of(sl) : 0;
-      int incl = nt;
+      const int nu = s < p.S ? units_of(sl) : 0;
+      int incl = nu;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
         if (lane >= o) incl += up;
       }
-      const int mine = base + (incl - nt) * HR;
-      const bool here = s < p.S && (r.per_item ? s == s_item : (r.t_begin >= mine && r.t_begin < mine + nt * HR));
+      const int mine = base + (incl - nu) * HR;
+      const bool here = s < p.S && (r.per_item ? s == s_item : (r.t_begin >= mine && r.t_begin < mine + nu * HR));
       const unsigned hit = __ballot_sync(0xFFFFFFFFu, here);
       if (hit) {
         const int src = __ffs(hit) - 1;
@@ -137,7 +139,8 @@ __device__ __forceinline__ void find_range(const QDecodeParams& p, Range* out) {
         r.base = __shfl_sync(0xFFFFFFFFu, mine, src);
         r.sl = __shfl_sync(0xFFFFFFFFu, sl, src);
         if (r.per_item) {  // this CTA's even part of its item
-          const int tiles = tiles_of(r.sl), t0 = r.base + (item - s_item * HR) * tiles, k = c - item * r.per_item;
+          const int tiles = tiles_of(r.sl), k = c - item * r.per_item;
+          const int t0 = r.base + (item - s_item * HR) * units_of(r.sl) + kQItemUnits;
           const int parts = min(r.per_item, tiles);  // the last CTAs of a short item have none
           if (k < parts) {
             r.t_begin = t0 + range_begin(k, tiles, parts);
@@ -157,7 +160,7 @@ struct Seg {
   int item, s, g, rg;
   int lo, hi;            // its tiles [lo, hi) of the item's nt
   int sl;                // session length
-  int item_t0;           // the item's first tile
+  int item_u0;           // the item's first unit
   int nt;
   int row_lo, rows;      // query rows [row_lo, row_lo + rows) of the N*G rows of this KV head
   int i_lo, n_ag;        // agents spanned by them
@@ -165,40 +168,44 @@ struct Seg {
 
 // Walks a CTA's range segment by segment.
 struct Walk {
-  int t, t_end, base, s, nt, sl;
+  int t, t_end, base, s, nu, sl;
   __device__ __forceinline__ void start(const Range& r) {
     t = r.t_begin;
     t_end = r.t_end;
     base = r.base;
     s = r.s;
     sl = r.sl;
-    nt = tiles_of(sl);
+    nu = units_of(sl);
   }
   __device__ __forceinline__ bool next(const QDecodeParams& p, Seg& sg) {
-    if (t >= t_end) return false;
     const int HR = p.Hkv * p.n_rg;
-    while (t >= base + nt * HR) {
-      base += nt * HR;
-      sl = session_len(p, ++s);
-      nt = tiles_of(sl);
+    for (;;) {
+      if (t >= t_end) return false;
+      while (t >= base + nu * HR) {
+        base += nu * HR;
+        sl = session_len(p, ++s);
+        nu = units_of(sl);
+      }
+      const int idx = (t - base) / nu, u0 = base + idx * nu;
+      const int end = min(t_end, u0 + nu);
+      sg.lo = max(t - u0 - kQItemUnits, 0);
+      sg.hi = end - u0 - kQItemUnits;
+      t = end;
+      if (sg.hi <= sg.lo) continue;  // only units that stand for the item's own cost
+      sg.s = s;
+      sg.sl = sl;
+      sg.nt = nu - kQItemUnits;
+      sg.item = s * HR + idx;
+      sg.item_u0 = u0;
+      sg.g = idx / p.n_rg;
+      sg.rg = idx - sg.g * p.n_rg;
+      sg.row_lo = sg.rg * p.rows_per_group;
+      const int row_hi = min(sg.row_lo + p.rows_per_group, p.rows_total);
+      sg.rows = row_hi - sg.row_lo;
+      sg.i_lo = sg.row_lo / p.G;
+      sg.n_ag = (row_hi - 1) / p.G - sg.i_lo + 1;
+      return true;
     }
-    const int idx = (t - base) / nt;
-    sg.lo = t - base - idx * nt;
-    sg.hi = min(nt, sg.lo + t_end - t);
-    sg.s = s;
-    sg.sl = sl;
-    sg.nt = nt;
-    sg.item = s * HR + idx;
-    sg.item_t0 = base + idx * nt;
-    sg.g = idx / p.n_rg;
-    sg.rg = idx - sg.g * p.n_rg;
-    sg.row_lo = sg.rg * p.rows_per_group;
-    const int row_hi = min(sg.row_lo + p.rows_per_group, p.rows_total);
-    sg.rows = row_hi - sg.row_lo;
-    sg.i_lo = sg.row_lo / p.G;
-    sg.n_ag = (row_hi - 1) / p.G - sg.i_lo + 1;
-    t += sg.hi - sg.lo;
-    return true;
   }
 };
 
@@ -888,8 +895,8 @@ __device__ __forceinline__ void q_sync() { named_bar_sync(1, kQThreads); }
 
 // Two records per CTA: 0 for the segment that starts the CTA's range, 1 for a later
 // one (only its last can be shared with the next CTA).
-__device__ __forceinline__ size_t q_record_slot(int cta, int cta_begin, int item_t0) {
-  return 2 * (size_t)cta + (item_t0 > cta_begin ? 1 : 0);
+__device__ __forceinline__ size_t q_record_slot(int cta, int cta_begin, int item_u0) {
+  return 2 * (size_t)cta + (item_u0 > cta_begin ? 1 : 0);
 }
 
 // Merge the warps' rows into the CTA's record rec = [m | l | O | Z] in shared
@@ -1033,10 +1040,10 @@ __device__ __forceinline__ void finish_item(const QDecodeParams& p, const Range&
       c_first = sg.item * range.per_item;
       segs = min(range.per_item, sg.nt);
     } else {
-      c_first = (int)owner_cta(sg.item_t0, W, C);
-      segs = (int)owner_cta(sg.item_t0 + sg.nt - 1, W, C) - c_first + 1;
+      c_first = (int)owner_cta(sg.item_u0 + kQItemUnits, W, C);
+      segs = (int)owner_cta(sg.item_u0 + kQItemUnits + sg.nt - 1, W, C) - c_first + 1;
     }
-    float* mine = p.partials + q_record_slot(blockIdx.x, range.t_begin, sg.item_t0) * REC;
+    float* mine = p.partials + q_record_slot(blockIdx.x, range.t_begin, sg.item_u0) * REC;
     for (int e = 4 * tid; e < REC; e += 4 * THREADS)
       __stcg(reinterpret_cast<float4*>(mine + e), *reinterpret_cast<const float4*>(rec + e));
     q_sync();
@@ -1051,7 +1058,7 @@ __device__ __forceinline__ void finish_item(const QDecodeParams& p, const Range&
     __threadfence();
     // Only the item's first CTA can hold it in its second record slot.
     const float* first =
-        p.partials + q_record_slot(c_first, range.per_item ? sg.item_t0 : range_begin(c_first, W, C), sg.item_t0) * REC;
+        p.partials + q_record_slot(c_first, range.per_item ? sg.item_u0 : range_begin(c_first, W, C), sg.item_u0) * REC;
     const float* rest = p.partials + 2 * (size_t)c_first * REC;
     auto record = [&](int j) { return j == 0 ? first : rest + (size_t)(2 * j) * REC; };
     for (int e = tid; e < segs * RP; e += THREADS) table[e] = __ldcg(record(e / RP) + e % RP);  // the records' m

@@ -66,7 +66,6 @@ struct QDecodeParams {
   int num_pages;
   int stages, u_stages;      // ring stages of K/V tiles and of U tiles
   int balance;               // visit an item's tiles in a low-discrepancy order (QOrder)
-  int slack;                 // see q_item_ctas
   float scale_log2;          // softmax_scale * log2(e)
   float* partials;           // two records per CTA: see q_record_slot
   int* tickets;              // one per work item
@@ -125,16 +124,25 @@ __host__ __device__ inline QDecodeSmem q_smem_plan(int D, int RK, int rows_block
 
 inline size_t q_record_floats(int RP, int D, int RK) { return (size_t)RP * (D + RK + 2); }
 
-constexpr int kQSlackTiles = 16;
+// What a stretch of an item costs a CTA beside its tiles (its queries, the merge of its
+// warps, publishing, finishing), in tiles: 5 to 7 us against 0.37 us for a tile at the
+// HBM rate.  The work is split in units: an item has its tiles and this many more.
+// (Without them a CTA whose share of the tiles was a handful of short or empty sessions
+// finished item after item long after the others: 24 ragged sessions 114 us.)
+constexpr int kQItemUnits = 16;
 
 // CTAs per item when every item takes the same number, or 0 for the even split of all
-// tiles.  Aligned shares end where items end: a CTA then finishes one stretch of one
-// item, where the even split's CTAs mostly finish two (and a CTA that holds a whole item
-// has nothing to publish or merge).  They are taken when the longest share is at most
-// `slack` tiles above the even one.
-__host__ __device__ inline int q_item_ctas(int items, int ctas, int nt_max, int W, int slack) {
-  const int k = items > 0 ? ctas / items : 0;
-  return k > 0 && (nt_max + k - 1) / k <= (W + ctas - 1) / ctas + slack ? k : 0;
+// units (W) over the CTAs.  Aligned shares end where items end: a CTA then has one
+// stretch of one item, where the even split's CTAs mostly have two (and a CTA that holds
+// a whole item has nothing to publish or merge).  They are taken when their longest is no
+// more than the even share, which has its item's units in it; of them the fewest CTAs
+// per item that lengthen the share by no more than another stretch costs.
+__host__ __device__ inline int q_item_ctas(int items, int ctas, int nt_max, int W) {
+  const int most = items > 0 ? ctas / items : 0;
+  if (most == 0) return 0;
+  const int share = (nt_max + most - 1) / most;
+  if (share > (W + ctas - 1) / ctas) return 0;
+  return (nt_max + share + kQItemUnits - 1) / (share + kQItemUnits);
 }
 
 lrkv_status launch_decode_quant(const QDecodeParams& p, int D, int RK, int rows, int fmt, const void* tmK,

@@ -120,7 +120,7 @@ lrkv_status plan_decode_quant(const lrkv_problem* p, int max_seq_len, const Devi
   pl->nt = max_seq_len > 0 ? (int)(((long long)max_seq_len + LRKV_QUANT_BLOCK - 1) / LRKV_QUANT_BLOCK) : 1;
   const long long per_session = (long long)p->num_kv_heads * pl->n_rg;
   pl->items = p->num_sessions * per_session;
-  if (pl->items > 0x3FFFFFFF || pl->items * pl->nt > 0x7FFF0000)
+  if (pl->items > 0x3FFFFFFF || pl->items * (pl->nt + lrkv::kQItemUnits) > 0x7FFF0000)
     return fail(LRKV_ERR_UNSUPPORTED, "too many (session, KV head, row group) items or tiles");
   const int sms = dev.sms < 1 ? 148 : dev.sms > lrkv::kQMaxCtas ? lrkv::kQMaxCtas : dev.sms;
   const long long W = pl->items * pl->nt;
@@ -275,7 +275,6 @@ lrkv_status lrkv_attn_decode_quant(const lrkv_problem* p, const void* q, const l
   dp.stages = pl.stages;
   dp.u_stages = pl.u_stages;
   dp.balance = p->mode == LRKV_BASE_SHARED;
-  dp.slack = lrkv::kQSlackTiles;
   dp.scale_log2 = scale_of(p) * 1.4426950408889634f;
   char* ws = static_cast<char*>(workspace);
   dp.flags = reinterpret_cast<unsigned*>(ws);
