@@ -18,7 +18,6 @@ namespace lrkv {
 
 namespace {
 
-constexpr int kThreads = 256;
 constexpr float kScaleMin = 7.888609052210118e-31f;  // 2^-100
 constexpr uint32_t kBf16Inf = 0x7F80u;
 
@@ -101,40 +100,49 @@ __device__ __forceinline__ float scale_need(float amax) {
   return fmaxf(s, kScaleMin);
 }
 
-// Codes of two values.  inv is 1 / scale, exact when the scale is a power of two.
+// Codes of eight values.  inv is 1 / scale, exact when the scale is a power of two
+// (pow2); `odd`: there may be infinities or NaN among them.
 template <int FMT>
-__device__ __forceinline__ uint32_t encode2(float a, float b, float scale, float inv, bool pow2) {
+__device__ __forceinline__ uint2 encode8(const float* f, float scale, float inv, bool pow2, bool odd) {
   if constexpr (FMT == LRKV_Q_E4M3) {
-    const float x = pow2 ? a * inv : __fdiv_rn(a, scale);
-    const float y = pow2 ? b * inv : __fdiv_rn(b, scale);
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(y), "f"(x));
-    return r;
-  } else {
-    // The nearest integer to x / scale: n = rint(x inv) is off by at most one, and
-    // the remainder r = x - n scale (one rounding; exact next to half a step)
-    // says so.  Of two equally near integers the even one.
-    uint32_t r = 0;
+    uint16_t r[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float x = i ? b : a;
-      float n = rintf(x * inv);
-      const float rem = fmaf(-n, scale, x);
-      const float twice = 2.f * fabsf(rem);
-      if (twice > scale || (twice == scale && (__float2int_rn(n) & 1))) n += copysignf(1.f, rem);
-      const int c = max(-127, min(127, __float2int_rn(n)));  // NaN gives 0
-      r |= (uint32_t)(c & 0xFF) << (8 * i);
+    for (int i = 0; i < 4; ++i) {
+      const float x = pow2 ? f[2 * i] * inv : __fdiv_rn(f[2 * i], scale);
+      const float y = pow2 ? f[2 * i + 1] * inv : __fdiv_rn(f[2 * i + 1], scale);
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r[i]) : "f"(y), "f"(x));
     }
-    return r;
+    return make_uint2((uint32_t)r[0] | (uint32_t)r[1] << 16, (uint32_t)r[2] | (uint32_t)r[3] << 16);
+  } else {
+    // The nearest integer to x / scale.  Adding 1.5 2^23 rounds x inv to an integer n and
+    // leaves it in the sum's low bits (with conversion instructions, a quarter of the
+    // rate, the 4 x 16k write took 139 us).  n is off by at most one, and the remainder
+    // x - n scale (one rounding; exact next to half a step) says so; of two equally near
+    // integers the even one.  That is rarely needed: one test for the eight values.
+    constexpr float kMagic = 12582912.f;
+    const float half = 0.5f * scale;
+    float t[8];
+    bool fix = odd;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      t[i] = fmaf(f[i], inv, kMagic);
+      fix |= fabsf(fmaf(kMagic - t[i], scale, f[i])) >= half;
+    }
+    if (fix) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float rem = fmaf(kMagic - t[i], scale, f[i]);
+        if (fabsf(rem) > half || (fabsf(rem) == half && (__float_as_uint(t[i]) & 1))) t[i] += copysignf(1.f, rem);
+        if (odd) t[i] = f[i] != f[i] ? kMagic : kMagic + fminf(fmaxf(t[i] - kMagic, -127.f), 127.f);
+      }
+    }
+    uint32_t n[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) n[i] = __float_as_uint(t[i]);
+    return make_uint2(
+        __byte_perm(__byte_perm(n[0], n[1], 0x0040), __byte_perm(n[2], n[3], 0x0040), 0x5410),
+        __byte_perm(__byte_perm(n[4], n[5], 0x0040), __byte_perm(n[6], n[7], 0x0040), 0x5410));
   }
-}
-
-template <int FMT>
-__device__ __forceinline__ uint2 encode8(const float* f, float scale, float inv, bool pow2) {
-  uint2 r;
-  r.x = encode2<FMT>(f[0], f[1], scale, inv, pow2) | encode2<FMT>(f[2], f[3], scale, inv, pow2) << 16;
-  r.y = encode2<FMT>(f[4], f[5], scale, inv, pow2) | encode2<FMT>(f[6], f[7], scale, inv, pow2) << 16;
-  return r;
 }
 
 __device__ __forceinline__ void bf16x8_to_f32(const uint4& v, float* f) {
@@ -159,7 +167,7 @@ __device__ __forceinline__ void decode4(uint32_t w, float* f) {
   f[code_byte<FMT>(3)] = b.y;
 }
 
-template <int FMT, int D>
+template <int FMT, int D, int kThreads>
 __global__ void __launch_bounds__(kThreads) quantize_kernel(const QCacheParams p) {
   constexpr int CPR = D / 8;                      // 16-byte chunks of a row
   constexpr int PER = kQBlock * CPR / kThreads;   // chunks of a thread
@@ -201,7 +209,8 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QCacheParams p
   if (__syncthreads_or(bad_page)) return;
 #pragma unroll
   for (int i = 0; i < kThreads / 32; ++i) top = max(top, red[i]);
-  if (top >= kBf16Inf) {  // the block holds an infinity or NaN: the largest finite magnitude
+  const bool odd = top >= kBf16Inf;
+  if (odd) {  // the block holds an infinity or NaN: the largest finite magnitude
     if (threadIdx.x == 0) atomicOr(p.flags, LRKV_DEVFLAG_NONFINITE);
     top = 0;
 #pragma unroll
@@ -231,7 +240,7 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QCacheParams p
     if (r < w.r0 || r >= w.r1) continue;
     float f[8];
     bf16x8_to_f32(v[i], f);
-    *reinterpret_cast<uint2*>(out + (long long)r * p.c_st + col) = encode8<FMT>(f, scale, inv, pow2);
+    *reinterpret_cast<uint2*>(out + (long long)r * p.c_st + col) = encode8<FMT>(f, scale, inv, pow2, odd);
   }
   if (w.r0 > 0 && scale == before) return;
   if (w.r0 > 0) {  // the scale grew: the block's older rows move to it
@@ -246,14 +255,15 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QCacheParams p
       decode4<FMT>(c.y, f + 4);
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] *= before;
-      *at = encode8<FMT>(f, scale, inv, pow2);
+      *at = encode8<FMT>(f, scale, inv, pow2, odd);
     }
   }
   if (threadIdx.x == 0) *scale_at = scale;  // every thread's `before` was read ahead of the barrier
 }
 
 template <int FMT, int D>
-__global__ void __launch_bounds__(kThreads) dequantize_kernel(const QCacheParams p) {
+__global__ void __launch_bounds__(256) dequantize_kernel(const QCacheParams p) {
+  constexpr int kThreads = 256;
   constexpr int CPR = D / 16;                     // 16-code chunks of a row
   constexpr int PER = kQBlock * CPR / kThreads;
   pdl_wait();
@@ -294,12 +304,12 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const QCacheParams
 }
 
 template <typename Kernel>
-lrkv_status launch(Kernel kern, const QCacheParams& p, void* stream) {
+lrkv_status launch(Kernel kern, int threads, const QCacheParams& p, void* stream) {
   const long long ctas = (long long)p.S * p.Hkv * 2 * p.nblk;
   if (ctas > 0x7FFFFFFFLL) return LRKV_ERR_UNSUPPORTED;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -309,22 +319,30 @@ lrkv_status launch(Kernel kern, const QCacheParams& p, void* stream) {
   return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? LRKV_OK : LRKV_ERR_CUDA;
 }
 
+// Threads of a writing CTA.  With many blocks, a block is 128 threads': more CTAs fit an SM and their loads and stores overlap (4 sessions x 16k x 8
+// heads: 105 us int8, 82 us e4m3, against 115 and 85 with 256 threads).  With few blocks
+// a block's own time counts, and 256 threads halve it (144 blocks: 3.1 us against 4.8).
+template <int FMT, int D>
+lrkv_status launch_quantize_fd(const QCacheParams& p, void* stream) {
+  const bool few = (long long)p.S * p.Hkv * 2 * p.nblk <= 296;
+  return few ? launch(quantize_kernel<FMT, D, 256>, 256, p, stream)
+             : launch(quantize_kernel<FMT, D, 128>, 128, p, stream);
+}
+
 }  // namespace
 
 lrkv_status launch_quantize(const QCacheParams& p, int D, int fmt, void* stream) {
   if (fmt == LRKV_Q_E4M3)
-    return D == 128 ? launch(quantize_kernel<LRKV_Q_E4M3, 128>, p, stream)
-                    : launch(quantize_kernel<LRKV_Q_E4M3, 64>, p, stream);
-  return D == 128 ? launch(quantize_kernel<LRKV_Q_INT8, 128>, p, stream)
-                  : launch(quantize_kernel<LRKV_Q_INT8, 64>, p, stream);
+    return D == 128 ? launch_quantize_fd<LRKV_Q_E4M3, 128>(p, stream) : launch_quantize_fd<LRKV_Q_E4M3, 64>(p, stream);
+  return D == 128 ? launch_quantize_fd<LRKV_Q_INT8, 128>(p, stream) : launch_quantize_fd<LRKV_Q_INT8, 64>(p, stream);
 }
 
 lrkv_status launch_dequantize(const QCacheParams& p, int D, int fmt, void* stream) {
   if (fmt == LRKV_Q_E4M3)
-    return D == 128 ? launch(dequantize_kernel<LRKV_Q_E4M3, 128>, p, stream)
-                    : launch(dequantize_kernel<LRKV_Q_E4M3, 64>, p, stream);
-  return D == 128 ? launch(dequantize_kernel<LRKV_Q_INT8, 128>, p, stream)
-                  : launch(dequantize_kernel<LRKV_Q_INT8, 64>, p, stream);
+    return D == 128 ? launch(dequantize_kernel<LRKV_Q_E4M3, 128>, 256, p, stream)
+                    : launch(dequantize_kernel<LRKV_Q_E4M3, 64>, 256, p, stream);
+  return D == 128 ? launch(dequantize_kernel<LRKV_Q_INT8, 128>, 256, p, stream)
+                  : launch(dequantize_kernel<LRKV_Q_INT8, 64>, 256, p, stream);
 }
 
 }  // namespace lrkv
