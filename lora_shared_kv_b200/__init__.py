@@ -224,6 +224,7 @@ def kv_view_dense(k, v):
     _on_device(k=k, v=v)
     view = KVView(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2), None, 0, 0, 0, 0)
     view.tensors = (k, v)  # a view keeps its tensors alive
+    view.holds = tuple(k.shape)
     return view
 
 
@@ -238,6 +239,7 @@ def kv_view_paged(k_pages, v_pages, page_table):
                   page_table.data_ptr(), page_table.stride(0), k_pages.stride(0), k_pages.shape[2],
                   k_pages.shape[0])
     view.tensors = (k_pages, v_pages, page_table)
+    view.holds = (page_table.shape[0], k_pages.shape[1], page_table.shape[1] * k_pages.shape[2], k_pages.shape[3])
     return view
 
 
@@ -286,12 +288,12 @@ def kv_view_quant_paged(k8_pages, v8_pages, k_scale, v_scale, page_table):
     return view
 
 
-def _quant_fits(view, problem, rows):
+def _fits(view, problem, rows, what):
     """The view's buffers hold the problem's sessions, KV heads and head_dim, and `rows` rows of each."""
     S, H, L, d = view.holds
     if S < problem.num_sessions or H < problem.num_kv_heads or L < rows or d != problem.head_dim:
         need = (problem.num_sessions, problem.num_kv_heads, int(rows), problem.head_dim)
-        raise ValueError(f"the 8-bit view holds [sessions, KV heads, rows, head_dim] {view.holds}, the call needs {need}")
+        raise ValueError(f"the {what} view holds [sessions, KV heads, rows, head_dim] {view.holds}, the call needs {need}")
 
 
 def u_view(u):
@@ -447,9 +449,11 @@ def lrkv_quantize_kv(problem, src, T, dst, dst_rows, first_rows, row_counts, wor
     """Write rows [0, n) of every session of the bf16 view `src` into rows [f, f + n) of the 8-bit view `dst`, which
     holds dst_rows rows a session: f = first_rows[s] (0 when None), n = row_counts[s] (T when None).  The cache then
     holds f + n tokens of the session."""
+    T, dst_rows = int(T), int(dst_rows)
     _rows_of(problem, first_rows, row_counts)
-    _quant_fits(dst, problem, dst_rows)
-    dev = _on_current(first_rows, row_counts, workspace, *dst.tensors)
+    _fits(src, problem, T, "bf16")
+    _fits(dst, problem, dst_rows, "8-bit")
+    dev = _on_current(first_rows, row_counts, workspace, *src.tensors, *dst.tensors)
     _check(lib().lrkv_quantize_kv(problem, src, T, dst, dst_rows, _at(first_rows), _at(row_counts),
                                   workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                   _raw_stream(stream, dev)))
@@ -458,9 +462,11 @@ def lrkv_quantize_kv(problem, src, T, dst, dst_rows, first_rows, row_counts, wor
 def lrkv_dequantize_kv(problem, src, src_rows, T, dst, first_rows, row_counts, workspace, stream=None):
     """Read rows [f, f + n) of every session of the 8-bit view `src` (src_rows rows a session) back into rows [0, n)
     of the bf16 view `dst`; f, n and T as in lrkv_quantize_kv."""
+    src_rows, T = int(src_rows), int(T)
     _rows_of(problem, first_rows, row_counts)
-    _quant_fits(src, problem, src_rows)
-    dev = _on_current(first_rows, row_counts, workspace, *src.tensors)
+    _fits(src, problem, src_rows, "8-bit")
+    _fits(dst, problem, T, "bf16")
+    dev = _on_current(first_rows, row_counts, workspace, *src.tensors, *dst.tensors)
     _check(lib().lrkv_dequantize_kv(problem, src, src_rows, T, dst, _at(first_rows), _at(row_counts),
                                     workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                     _raw_stream(stream, dev)))
@@ -489,7 +495,8 @@ def lrkv_attn_decode_quant(problem, q, kv, seq_lens, max_seq_len, u, b, offsets,
     _require(q.numel() >= size and out.numel() >= size, "q and out: [num_sessions, num_agents, num_q_heads, head_dim]")
     _require(b.numel() >= p.num_agents * p.rank * p.num_kv_heads * p.head_dim,
              "b: [num_agents, rank, num_kv_heads * head_dim]")
-    _quant_fits(kv, p, max_seq_len)
+    max_seq_len = int(max_seq_len)
+    _fits(kv, p, max_seq_len, "8-bit")
     dev = _on_current(q, seq_lens, b, offsets, out, workspace, *kv.tensors)
     uv = u if isinstance(u, UView) else u_view(u)
     _check(lib().lrkv_attn_decode_quant(p, q.data_ptr(), kv, seq_lens.data_ptr(), max_seq_len, uv, b.data_ptr(),

@@ -118,9 +118,10 @@ lrkv_status plan_decode_quant(const lrkv_problem* p, int max_seq_len, const Devi
   }
   pl->n_u_slots = p->mode == LRKV_BASE_SHARED ? max_ag : 1;
   pl->nt = max_seq_len > 0 ? (int)(((long long)max_seq_len + LRKV_QUANT_BLOCK - 1) / LRKV_QUANT_BLOCK) : 1;
+  if (p->num_kv_heads > 0xFFFF) return fail(LRKV_ERR_UNSUPPORTED, "%d KV heads", p->num_kv_heads);
   const long long per_session = (long long)p->num_kv_heads * pl->n_rg;
   pl->items = p->num_sessions * per_session;
-  if (pl->items > 0x3FFFFFFF || pl->items * (pl->nt + lrkv::kQItemUnits) > 0x7FFF0000)
+  if (pl->items > 0x3FFFFFF || pl->items * (pl->nt + lrkv::kQItemUnits) > 0x7FFF0000)
     return fail(LRKV_ERR_UNSUPPORTED, "too many (session, KV head, row group) items or tiles");
   const int sms = dev.sms < 1 ? 148 : dev.sms > lrkv::kQMaxCtas ? lrkv::kQMaxCtas : dev.sms;
   const long long W = pl->items * pl->nt;

@@ -378,6 +378,9 @@ SHAPES = [  # S, N, G, Hkv, d, r, L, mode, offsets, lens
     (1, 8, 8, 1, 128, 16, 200, 1, [0, 3, 64, 65, 128, 199, 200, 500], [200]),  # 64 rows
     (1, 3, 7, 2, 128, 8, 129, 0, [0, 128, 129], [129]),                  # 21 rows, rank 8
     (5, 1, 1, 3, 128, 16, 4097, 0, [0, 4000, 4096, 1, 64], [4097, 63, 0, 64, 65]),  # ragged
+    (1, 8, 2, 1, 128, 32, 1500, 0, [0, 1, 2, 3, 64, 700, 1400, 1499], [1500]),   # large U tiles: groups share stages
+    (1, 16, 1, 1, 128, 32, 1100, 0, list(range(0, 1040, 65)), [1100]),           # one U stage for every group
+    (41, 1, 2, 1, 64, 8, 150, 0, [(7 * i) % 160 for i in range(41)], [(i * 37) % 151 for i in range(41)]),  # 41 sessions
 ]
 
 
@@ -412,6 +415,50 @@ def test_paged_is_dense_bit_for_bit_and_runs_repeat():
     first = a.run(ws=ws)
     assert torch.equal(first, a.run(ws=ws))
     assert torch.equal(first, b.run())
+
+
+def test_sessions_that_share_pages():
+    """Two sessions whose page tables begin with the same pages, and a page that a table names twice."""
+    c = DecodeCase("share", "e4m3", 2, 2, 2, 2, 128, 16, 320, 0, [0, 64, 0, 64], [320, 320], paged=True)
+    c.cache.table[1, :3] = c.cache.table[0, :3]
+    c.cache.table[1, 4] = c.cache.table[1, 3]
+    c.cache.table_cpu = c.cache.table.cpu()
+    c.check(c.run(), "shared pages")
+
+
+def test_two_streams_with_their_own_workspaces():
+    a = DecodeCase("stream a", "e4m3", 2, 3, 2, 2, 128, 16, 2000, 0, [0, 900, 1999, 7, 64, 65], [2000, 1500])
+    b = DecodeCase("stream b", "int8", 3, 2, 4, 1, 64, 32, 1700, 1, [0, 5, 0, 0, 1, 2], [1700, 3, 900], paged=True)
+    want = [a.run(), b.run()]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    spaces = [a.workspace(), b.workspace()]
+    torch.cuda.synchronize()
+    outs = []
+    for i in range(6):
+        for case, st, ws in zip((a, b), streams, spaces):
+            with torch.cuda.stream(st):
+                outs.append(case.run(ws=ws, check=False))
+    torch.cuda.synchronize()
+    for i, out in enumerate(outs):
+        assert torch.equal(out, want[i % 2])
+    assert all(lrkv.lrkv_query_device_status(ws)[0] == "LRKV_OK" for ws in spaces)
+
+
+def test_views_too_small_are_refused():
+    c = DecodeCase("small", "int8", 2, 2, 2, 2, 64, 16, 100, 0, [0, 0, 0, 0], [100, 100])
+    c.L = 101
+    with pytest.raises(ValueError, match="8-bit view holds"):
+        lrkv.lrkv_attn_decode_quant(c.problem, c.q, c.cache.view(), _i32(c.lens), 101, c.u, c.b, None,
+                                    torch.empty_like(c.q), c.workspace())
+    k = _tokens("small", 2, 5, 2, 64)
+    with pytest.raises(ValueError, match="bf16 view holds"):
+        c.cache.write(k, k, 6, None, None)
+    wide = lrkv.make_problem(2, 1, 3, 3, 64, 16)
+    src = lrkv.kv_view_dense(k.permute(0, 2, 1, 3), k.permute(0, 2, 1, 3))
+    with pytest.raises(ValueError, match="view holds"):
+        lrkv.lrkv_dequantize_kv(wide, c.cache.view(), 100, 5, src, None, None, _flags_ws())
+    with pytest.raises(ValueError, match="int32"):
+        lrkv.lrkv_quantize_kv(c.problem, src, 5, c.cache.view(), 100, _i32([0, 0]).long(), None, _flags_ws())
 
 
 def test_null_offsets_are_zero():
