@@ -8,12 +8,17 @@
 // the same reordered form as over a bf16 cache: the rank-r product is accumulated
 // per row and B_i applied once.
 //
-//  * What bounds it: the codes are read once from HBM, 2 d bytes a key and head,
-//    half a bf16 cache's.  At that rate an SM gets a 64-key tile (16 KB at d =
-//    128) every 730 cycles, and has to turn its 16 K codes into fp16 (the tensor
-//    cores' fp8 form is no faster for warp-level MMAs here, and would round q
-//    and p to 4 bits): a conversion per two codes at half rate, 128 cycles, and
-//    per 16 rows 128 MMAs of m16n8k16 at 2 cycles, 256 cycles.
+//  * What bounds it: the codes are read once from HBM, 2 d bytes a key and head, half
+//    a bf16 cache's.  At that rate an SM gets a 64-key tile (16 KB at d = 128) every
+//    730 cycles, and has to turn its 16 K codes into fp16: a conversion per two codes
+//    at half rate, 128 cycles, and per 16 rows 128 MMAs of m16n8k16 at 2 cycles, 256
+//    cycles.  (The warp-level fp8 MMA measured 6.2 cycles against 3.3 for fp16 MMA and
+//    conversions together, and would round q and p to 4 bits.)  Measured: 4 x 64k paged,
+//    8 agents, 117 us (floor 85); 32 x 8k, 18 rows, e4m3 53 us and int8 58 (floor 21);
+//    16 x 1k, 4 rows, 14.8 us (floor 5.3).  A launch takes about 7 us until its first
+//    tile has landed and 4 to 7 us from the last tile to the output, which is what
+//    separates the shorter ones from their floor; at 18 rows the warps' latency chains
+//    (3,000 cycles for 32 keys) hold the ring as well.
 //  * A warp holds ALL rows of its row block (8, 16 or 16 + 8) and a slice of the
 //    tile's keys, so that a code is converted once per tile.  The 16-row part
 //    has rows as the MMA's M, the 8-row part has keys (or dims) as M; the
@@ -34,7 +39,8 @@
 //    split evenly over the CTAs (each counts the sessions' tiles at its start), so
 //    ragged batches are balanced; an item cut between CTAs is merged by the last one
 //    to finish.
-//  * Keys past seq_len and U rows before a_i are removed by selects on operands.
+//  * Scores past seq_len and U rows before a_i are removed by selects on operands,
+//    value codes past seq_len by zeroing them in shared memory.
 #pragma once
 
 #include <float.h>

@@ -4,7 +4,9 @@
 //           code = round(x / scale')
 //   read    y = bf16(code * scale)
 //
-// Both are bound by memory: 3 bytes move per element.  One CTA takes one block of
+// Both are bound by memory: 3 bytes move per element (4 sessions x 16k x 8 heads written
+// whole: floor 62 us, e4m3 82, int8 106, whose rounding still costs instructions; 16k x 8
+// heads read back: floor 15 us, 20).  One CTA takes one block of
 // one (session, KV head) of K or of V: 64 tokens x head_dim, at most 16 KB of
 // bf16, which stays in registers between the block's maximum and its rounding,
 // so every element is read once.
