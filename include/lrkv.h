@@ -475,6 +475,8 @@ size_t lrkv_decode_quant_workspace_bytes(const lrkv_problem* p, int32_t max_seq_
  * against a running reference, so no weight of a long context underflows) and
  * the low-rank product as bf16.  Codes, scales and U rows at or past seq_len and U
  * rows before a_i may hold anything, NaN included.
+ * A NaN or infinity in a U row that counts for one agent may reach the outputs of
+ * other agents of the call, as in lrkv_attn_decode.
  * Ragged batches are split over the SMs by their actual lengths.
  */
 lrkv_status lrkv_attn_decode_quant(const lrkv_problem* p, const void* q, const lrkv_qkv_view* kv,

@@ -79,7 +79,7 @@ struct __align__(16) Entry {
   int session;
   float ks, vs;  // the block's scales
   int u;         // agents whose U tile is copied (16 bits) | U stage << 16 | its phase << 24; 0: none
-  int n;         // number of the tile among the CTA's
+  int pad;
 };
 constexpr int kBadTile = -1, kNoTile = -2;
 constexpr int kPlan = 32;   // tiles of a planned chunk
@@ -360,7 +360,6 @@ __device__ __forceinline__ void q_plan(const QDecodeParams& p, const QBars& bar,
         e->head = sg.g | sg.i_lo << 16;
         e->session = sg.s;
         e->u = need ? (int)need | us << 16 | (use & 1) << 24 : 0;
-        e->n = n + lane;
       }
       const bool filled = slot + m == kPlan;
       __syncwarp();

@@ -89,6 +89,7 @@ __host__ __device__ constexpr QShape q_shape(int rows) {
   return rows <= 8 ? QShape{0, 1, 1} : rows <= 16 ? QShape{1, 0, 1} : rows <= 24 ? QShape{1, 1, 1} : QShape{1, 0, 2};
 }
 
+// Groups of warps that take a CTA's tiles in turn.
 __host__ __device__ constexpr int q_groups(int nrb) { return kQWarps / (kQBlock / kQWarpKeys) / nrb; }
 
 // Accumulator fragments that the warps exchange per pass when their rows are merged.
@@ -109,7 +110,7 @@ __host__ __device__ inline QDecodeSmem q_smem_plan(int D, int RK, int rows_block
   s.u_bytes = n_u_slots * kQBlock * RK * 2;
   s.u_off = stages * s.tile_bytes;
   s.rec_off = s.u_off + u_stages * s.u_bytes;                            // [m | l | O | Z] of RP rows
-  s.mb_off = round_up(s.rec_off + RP * (D + RK + 2) * 4, 16);                        // the warps' fragments, then the records' scales
+  s.mb_off = round_up(s.rec_off + RP * (D + RK + 2) * 4, 16);            // the warps' fragments; the records' scales
   const int mb_bytes = kQWarps * kQMergeFrags * 512, table_bytes = kQMaxCtas * RP * 4;
   s.ml_off = s.mb_off + (mb_bytes > table_bytes ? mb_bytes : table_bytes);  // the warps' m and l
   s.q_off = round_up(s.ml_off + kQWarps * rows_block * 2 * 4, 16);       // 24-row blocks: query fragments
