@@ -14,7 +14,7 @@
 //    at half rate, 128 cycles, and per 16 rows 128 MMAs of m16n8k16 at 2 cycles, 256
 //    cycles.  (The warp-level fp8 MMA measured 6.2 cycles against 3.3 for fp16 MMA and
 //    conversions together, and would round q and p to 4 bits.)  Measured: 4 x 64k paged,
-//    8 agents, 117 us (floor 85); 32 x 8k, 18 rows, e4m3 53 us and int8 58 (floor 21);
+//    8 agents, 117 us (floor 85); 32 x 8k, 18 rows, e4m3 52 us and int8 58 (floor 21);
 //    16 x 1k, 4 rows, 14.8 us (floor 5.3).  A launch takes about 7 us until its first
 //    tile has landed and 4 to 7 us from the last tile to the output, which is what
 //    separates the shorter ones from their floor; at 18 rows the warps' latency chains

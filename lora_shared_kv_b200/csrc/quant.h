@@ -131,18 +131,21 @@ inline size_t q_record_floats(int RP, int D, int RK) { return (size_t)RP * (D + 
 // (Without them a CTA whose share of the tiles was a handful of short or empty sessions
 // finished item after item long after the others: 24 ragged sessions 114 us.)
 constexpr int kQItemUnits = 16;
+// Tiles by which an aligned share may exceed the even one, which ends inside items more
+// often than it counts (128 items of 128 tiles: 60.3 us aligned, 63.1 even).
+constexpr int kQAlignTiles = 4;
 
 // CTAs per item when every item takes the same number, or 0 for the even split of all
 // units (W) over the CTAs.  Aligned shares end where items end: a CTA then has one
 // stretch of one item, where the even split's CTAs mostly have two (and a CTA that holds
-// a whole item has nothing to publish or merge).  They are taken when their longest is no
-// more than the even share, which has its item's units in it; of them the fewest CTAs
-// per item that lengthen the share by no more than another stretch costs.
+// a whole item has nothing to publish or merge).  They are taken when their longest is at
+// most kQAlignTiles above the even share, which has its item's units in it; of them the
+// fewest CTAs per item that lengthen the share by no more than another stretch costs.
 __host__ __device__ inline int q_item_ctas(int items, int ctas, int nt_max, int W) {
   const int most = items > 0 ? ctas / items : 0;
   if (most == 0) return 0;
   const int share = (nt_max + most - 1) / most;
-  if (share > (W + ctas - 1) / ctas) return 0;
+  if (share > (W + ctas - 1) / ctas + kQAlignTiles) return 0;
   return (nt_max + share + kQItemUnits - 1) / (share + kQItemUnits);
 }
 

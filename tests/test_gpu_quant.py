@@ -461,6 +461,28 @@ def test_views_too_small_are_refused():
         lrkv.lrkv_quantize_kv(c.problem, src, 5, c.cache.view(), 100, _i32([0, 0]).long(), None, _flags_ws())
 
 
+def test_no_tokens_at_all_and_bounds_below_the_cache():
+    c = DecodeCase("none", "e4m3", 2, 2, 2, 2, 64, 16, 300, 0, [0, 0, 0, 0], [300, 200])
+    c.lens, c.L = [0, 0], 0
+    assert (c.run() == 0).all()
+    c.lens, c.L = [70, 0], 100  # the bound is the call's, not the cache's
+    c.check(c.run(), "bound below the cache")
+
+
+def test_every_code_enters_as_the_number_it_is():
+    for fmt in ("int8", "e4m3"):  # int8's -128 is not written, but read
+        c = DecodeCase("codes", fmt, 1, 1, 4, 1, 128, 16, 192, 0, [192], [192])
+        codes = torch.arange(256, dtype=torch.int32).to(torch.uint8)
+        if fmt == "e4m3":
+            codes = codes[(codes & 0x7F) != 0x7F]  # without the NaNs
+        n = 192 * 128
+        for i, t in enumerate((c.cache.k, c.cache.v)):
+            t.view(torch.uint8).copy_(codes.repeat(n // codes.numel() + 1)[i:i + n].view(1, 1, 192, 128).to(DEV))
+        c.cache.ks[:] = 2.0 ** -7 if fmt == "int8" else 2.0 ** -9
+        c.cache.vs[:] = 2.0 ** -5
+        c.check(c.run(), fmt)
+
+
 def test_null_offsets_are_zero():
     c = DecodeCase("null", "e4m3", 2, 2, 2, 2, 128, 16, 333, 0, [0, 0, 0, 0], [333, 200])
     assert torch.equal(c.run(), c.run(offsets=False))
