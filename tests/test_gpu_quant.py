@@ -518,7 +518,8 @@ def test_a_sink_and_a_long_flat_tail():
 
 
 def test_large_scores_and_queries():
-    # scores of a few hundred: exponents off by 128 * 2^-24 * |s|, so that the bound's share grows with them
+    # sum |q k| scale is about 128 * 24 * 0.8 / 11.3 = 217 here: an exponent is off by at most 128 * 217 * 2^-24 =
+    # 1.7e-3, twice that where the tensor cores truncate, and again for the denominator: 6.6e-3 = 27 * 2^-12
     c = DecodeCase("large", "int8", 1, 2, 4, 1, 128, 16, 300, 0, [0, 150], [300], q_std=30.0)
     c.check(c.run(), "large", weight=40.0)
     for f in (2.0 ** 100, 2.0 ** -100):  # the queries' own size cancels against the softmax scale
