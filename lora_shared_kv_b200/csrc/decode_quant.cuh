@@ -594,8 +594,7 @@ __device__ __forceinline__ int slot_key(int s) { return s ^ ((s & 8) >> 1); }
 // weights for the low-rank product are left in pz (of each 16 keys and eight rows, as
 // a B fragment) if want_z.
 // A tile that reaches past seq_len: its value codes past it are zeroed in shared memory
-// first, and its scores past it selected out.  (One path for every tile: two instances
-// of this code cost a copy of every accumulator where they meet.)
+// first, and its scores past it selected out, so that one path serves every tile.
 template <int FMT, int D, int RK, int H16, int H8>
 __device__ __forceinline__ void q_tile(WarpRows<D, RK, H16, H8>& st, int sl, uint32_t Ks, float ks_scale,
                                        float vs_scale, int key0, int kw, const uint32_t* qs, bool want_z,
