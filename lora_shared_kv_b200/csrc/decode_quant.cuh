@@ -697,7 +697,11 @@ __device__ __forceinline__ void q_tile(WarpRows<D, RK, H16, H8>& st, int sl, uin
   float sc[NR], mx[NR];
 #pragma unroll
   for (int i = 0; i < NR; ++i) {
+    // A key scale may be zero, or take the product below fp32 (a block of zero keys is
+    // written with 2^-100): the factor stays positive then, or the -inf of a masked score
+    // would turn into NaN.  Raw scores end at 2^31, so they still come out under 2^-94.
     sc[i] = st.c[i] * ks_scale;
+    sc[i] = sc[i] < FLT_MIN ? FLT_MIN : sc[i];
     mx[i] = kNegInf;
   }
 #pragma unroll
@@ -713,7 +717,7 @@ __device__ __forceinline__ void q_tile(WarpRows<D, RK, H16, H8>& st, int sl, uin
       for (int i = 0; i < 2; ++i) mx[R8 + i] = max3(mx[R8 + i], s8[nb][i], s8[nb][2 + i]);
     }
   }
-  // The scale is >= 0 and rounding monotonic: the scaled maximum is the maximum of
+  // The factor is > 0 and rounding monotonic: the scaled maximum is the maximum of
   // the scaled scores.  Each lane checks its own keys; the lanes of a row agree on
   // a new reference only on the few tiles that need one.
   const float lvs = __log2f(vs_scale);
