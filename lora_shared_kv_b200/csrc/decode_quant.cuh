@@ -33,8 +33,10 @@
 //    The weights enter the value product as fp16, times the block's value scale:
 //    p' = p 2^(m - w) sv, with a second reference w per row that keeps the largest
 //    p' between 2^8 and 2^15 (fp16 ends at 2^16 and is full-precision down to
-//    2^-14).  So p' carries 11 bits down to 2^-22 of the largest weight and 2^-33
-//    absolute, whatever the scales.  The low-rank product takes p as bf16.
+//    2^-14).  So p' carries 11 bits down to 2^-22 of the largest p' and 2^-33
+//    absolute, whatever the scales; where the largest p' belongs to keys whose p is
+//    under 2^-119 of the row's largest, it may be as low as 2^1 (the factor 2^(m - w) sv
+//    ends at 2^127).  A p below 2^-126 is zero.  The low-rank product takes p as bf16.
 //  * The items' tiles of the actual lengths, and what an item costs beside them, are
 //    split evenly over the CTAs (each counts the sessions' tiles at its start), so
 //    ragged batches are balanced; an item cut between CTAs is merged by the last one
@@ -725,7 +727,8 @@ __device__ __forceinline__ void q_tile(WarpRows<D, RK, H16, H8>& st, int sl, uin
 #pragma unroll
   for (int i = 0; i < NR; ++i) {
     mx[i] *= sc[i];
-    need |= mx[i] > fminf(st.m[i] + 8.f, st.w[i] + 15.f - lvs);
+    const float a = st.w[i] - lvs;
+    need |= mx[i] > (a < st.m[i] - 127.f ? st.m[i] - 126.f : fminf(st.m[i] + 8.f, a + 15.f));
   }
   if (__any_sync(0xFFFFFFFFu, need)) {
     float al[NR], be[NR];
@@ -737,8 +740,12 @@ __device__ __forceinline__ void q_tile(WarpRows<D, RK, H16, H8>& st, int sl, uin
       const float mn = fmaxf(st.m[i], mx[i]);
       al[i] = mn == kNegInf ? 1.f : fast_exp2(st.m[i] - mn);
       st.m[i] = mn;
+      // w: top is the tile's largest p' in log2 units; 2^(m - w) sv stays within 2^127.
+      // Where m - w would pass that, the largest p' is still 2^1 or more (w <= top - 1,
+      // since mx >= m - 126).  Weights below 2^-126 are zero and move nothing.
       const float top = mx[i] + lvs;
-      const float wn = top > st.w[i] + 15.f ? top - 8.f : st.w[i];
+      float wn = st.w[i];
+      if (mx[i] >= mn - 126.f) wn = fmaxf(top > wn + 15.f ? top - 8.f : wn, mn + lvs - 127.f);
       be[i] = wn == kNegInf ? 1.f : fast_exp2(st.w[i] - wn);
       st.w[i] = wn;
       st.l[i] *= al[i];
@@ -772,7 +779,9 @@ __device__ __forceinline__ void q_tile(WarpRows<D, RK, H16, H8>& st, int sl, uin
 #pragma unroll
   for (int i = 0; i < NR; ++i) {
     mu[i] = st.m[i] == kNegInf ? 0.f : st.m[i];
-    f[i] = fast_exp2(mu[i] - (st.w[i] == kNegInf ? 0.f : st.w[i]) + lvs);  // 2^(m - w) sv
+    // 2^(m - w) sv; past 2^127 only where every weight of this row and tile is zero
+    const float e = mu[i] - (st.w[i] == kNegInf ? 0.f : st.w[i]) + lvs;
+    f[i] = fast_exp2(e > 127.f ? 127.f : e);
   }
   // weights: pz (bf16) for the low-rank product, pv (fp16, scaled) for the values
   uint32_t pv16[H16 ? NB : 1][4], pv8[H8 ? NB : 1][2];

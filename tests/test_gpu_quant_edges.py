@@ -69,3 +69,77 @@ def test_zero_keys_as_written_and_tiny_queries(fmt, rows):
         for s, n in enumerate(lens):
             assert (c.cache.logical("k")[1][s, :, (n - 1) // 64] == 2.0 ** -100).all()
         _check(c, c.run(), lens)
+
+
+# ---------------------------------------------------------------------------
+# value scales that are zero or far from those of a row's largest scores
+# ---------------------------------------------------------------------------
+
+def _sink(c, at, gap):
+    """Give every row of c one key, `at`, whose score lies `gap` above the others' (which are all zero)."""
+    S, L, H, d = c.cache.S, c.cache.rows, c.cache.Hkv, c.cache.d
+    c.q[:] = 1.0
+    k = torch.zeros((S, L, H, d), dtype=torch.bfloat16, device=DEV)
+    k[:, at] = gap / d ** 0.5
+    c.cache.write(k, _tokens("sink v", S, L, H, d), L, None, _i32(c.lens))
+
+
+def _clear_values(c, blocks, zero_scale):
+    """Zero values in these blocks: as the write leaves them, or with a scale of zero."""
+    if zero_scale:
+        c.cache.vs[:, :, blocks] = 0
+    else:
+        for j in blocks:
+            c.cache.v[:, :, 64 * j:64 * j + 64].view(torch.uint8).zero_()
+            c.cache.vs[:, :, j] = 2.0 ** -100
+
+
+@pytest.mark.parametrize("rows", ROWS, ids=str)
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_a_sink_whose_block_holds_no_values(fmt, rows):
+    """The block of a row's far largest score has values of zero: the others' small weights are all of the output.
+    Their largest weight times its scale is brought to 2^1 or more (2^8 where it lies within 2^-119 of the largest
+    weight), so fp16's absolute half step of 2^-25 is 2^-26 of it."""
+    N, G = rows
+    for gap in (20.0, 78.0, 82.0, 85.0, 87.0, 90.0):
+        for zero_scale in (True, False):
+            for big in (0, 60, 100):  # other blocks' value scales up to 2^100
+                c = DecodeCase(("sv", fmt, rows), fmt, 2, N, G, 1, 128, 16, 330, 0, [400] * (2 * N), [330, 270],
+                               b_std=0.0, poison=False)
+                _sink(c, 3, gap)
+                c.cache.vs[:] = torch.exp2(torch.tensor([0.0, big, big - 8, big, big - 30, big - 3], device=DEV))
+                _clear_values(c, [0], zero_scale)
+                _check(c, c.run(), (gap, zero_scale, big), weight=12.0, floor=2.0 ** -26)
+
+
+@pytest.mark.parametrize("rows", ROWS, ids=str)
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_no_values_until_a_short_last_block(fmt, rows):
+    """Zero values, then a last block of so few keys that half of its tile is past the end: large scores, and value
+    scales 2^100 and more apart."""
+    N, G = rows
+    for lens in ([321, 286], [257, 342], [352, 353]):  # 5 or 6 tiles: a warp takes the last one and an earlier one
+        for size, scale in ((3.0, 1.0), (1.0, 2.0 ** 60), (0.0, 2.0 ** 100)):
+            for zero_scale in (True, False):
+                c = DecodeCase(("lv", fmt, rows, lens), fmt, 2, N, G, 2, 64, 8, 384, 1, [0] * (2 * N), lens, b_std=0.0)
+                c.q[:] = 1.0
+                k = torch.full((2, 384, 2, 64), size * 12.0, dtype=torch.bfloat16, device=DEV)  # 96 * size a score
+                c.cache.write(k, _tokens("lv v", 2, 384, 2, 64), 384, None, _i32(lens))
+                last = [(n - 1) // 64 for n in lens]
+                c.cache.vs[:] = scale
+                for s, j in enumerate(last):
+                    one = DecodeCase.__new__(DecodeCase)
+                    one.cache = type("Part", (), dict(v=c.cache.v[s:s + 1], vs=c.cache.vs[s:s + 1]))
+                    _clear_values(one, list(range(j)), zero_scale)
+                # scores up to 288: 4 * 128 * 288 * 2^-24 = 36 * 2^-12
+                _check(c, c.run(), (lens, size, scale, zero_scale), weight=36.0)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_zero_values_as_written_before_large_ones(fmt):
+    """All through the write: blocks of zeros (scale 2^-100), then 20 rows of about 2^30."""
+    c = DecodeCase(("wr", fmt), fmt, 1, 2, 4, 1, 128, 16, 384, 0, [340, 340], [340], b_std=0.0)
+    v = torch.zeros((1, 384, 1, 128), dtype=torch.bfloat16, device=DEV)
+    v[:, 320:] = _tokens("wr v", 1, 64, 1, 128) * 2.0 ** 30
+    c.cache.write(_tokens("wr k", 1, 384, 1, 128), v, 384, None, _i32([340]))
+    _check(c, c.run(), fmt)
