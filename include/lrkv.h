@@ -200,7 +200,9 @@ size_t lrkv_decode_workspace_bytes(const lrkv_problem* p, int32_t max_seq_len);
  *   out            device [S, N, Hq, d] contiguous, bf16 or fp32 (out_dtype)
  *   workspace      device, >= lrkv_decode_workspace_bytes(p, max_seq_len),
  *                  16-byte aligned, zero-filled once before its first use
- *                  (lrkv_workspace_reset); every call leaves it reusable.
+ *                  (lrkv_workspace_reset); every call leaves it reusable by
+ *                  calls of the same shape (S, N, Hq, Hkv, d, r): reset it
+ *                  before one of another shape or after another operator.
  *                  Calls that share a workspace must be ordered (same stream).
  * A session with seq_len 0 gets a zero output.
  */
@@ -312,7 +314,8 @@ size_t lrkv_prefill_workspace_bytes(const lrkv_problem* p, int32_t ctx_len, int3
  *   out            device [N, T, Hq, d] contiguous, bf16 or fp32
  *   workspace      device, >= lrkv_prefill_workspace_bytes, zero-filled once
  *                  (the tickets return to zero by the end of every call; calls
- *                  sharing a workspace must be ordered on one stream)
+ *                  sharing a workspace must be ordered on one stream; reset it
+ *                  before a call with more rows, or after a decode)
  */
 lrkv_status lrkv_attn_prefill_chunk(const lrkv_problem* p, const void* q, const lrkv_kv_view* kv,
                                     int32_t session, int32_t ctx_len, int32_t T,
@@ -461,7 +464,11 @@ lrkv_status lrkv_dequantize_kv(const lrkv_problem* p, const lrkv_qkv_view* src, 
                                void* workspace, size_t workspace_bytes, lrkv_stream_t stream);
 
 /* Bytes of workspace lrkv_attn_decode_quant needs (whatever the lengths up to
- * max_seq_len); 0 if the call would refuse the shape. */
+ * max_seq_len); 0 if the call would refuse the shape.  One workspace, zero-filled
+ * once and large enough for each, may serve calls of different shapes, and calls
+ * of the other operators before them, in stream order.  (lrkv_attn_decode and
+ * lrkv_attn_prefill_chunk want theirs reset where the shape changes, or after a
+ * decode over 8 bits.) */
 size_t lrkv_decode_quant_workspace_bytes(const lrkv_problem* p, int32_t max_seq_len);
 
 /*

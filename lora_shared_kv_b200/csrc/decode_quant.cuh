@@ -1066,8 +1066,10 @@ __device__ __forceinline__ void finish_item(const QDecodeParams& p, const Range&
     q_sync();
     if (tid == 0) {
       __threadfence();
-      const int last = atomicAdd(p.tickets + sg.item, 1) == segs - 1;
-      if (last) p.tickets[sg.item] = 0;
+      unsigned* word = p.tickets + (c_first >> 2);  // c_first's byte of it
+      const int at = 8 * (c_first & 3);
+      const int last = (int)(atomicAdd(word, 1u << at) >> at & 0xFF) == segs - 1;
+      if (last) atomicSub(word, (unsigned)segs << at);
       *bcast = last;
     }
     q_sync();

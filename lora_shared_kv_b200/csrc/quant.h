@@ -68,7 +68,7 @@ struct QDecodeParams {
   int balance;               // visit an item's tiles in a low-discrepancy order (QOrder)
   float scale_log2;          // softmax_scale * log2(e)
   float* partials;           // two records per CTA: see q_record_slot
-  int* tickets;              // one per work item
+  unsigned* tickets;         // a byte per CTA: see kQTicketBytes
   unsigned* flags;
   unsigned spin_cap;         // failure-detection test hook, as in DecodeParams
   int stall;
@@ -95,6 +95,13 @@ __host__ __device__ constexpr int q_groups(int nrb) { return kQWarps / (kQBlock 
 // Accumulator fragments that the warps exchange per pass when their rows are merged.
 constexpr int kQMergeFrags = 4;
 constexpr int kQMaxCtas = 160;  // CTAs of a launch at most (and so partial records of an item)
+// Tickets of the items that are cut between CTAs, between the status header and the
+// records.  An item counts in the byte of its first CTA (no two cut items share that one:
+// of two, the earlier would end in it), so their place depends on no shape, and a
+// workspace that served other shapes holds zeros there.  The other operators' workspaces
+// keep their first tickets at these bytes, zero between calls as well.
+constexpr int kQTicketBytes = 256;
+static_assert(kQMaxCtas <= kQTicketBytes && kQMaxCtas < 256, "a byte counts the CTAs of an item");
 constexpr int kQPlanBytes = 4 * 32 * 32, kQPlanBarriers = 12;  // the planner's table of tiles
 
 // Shared-memory plan (bytes from a 1024-aligned base).

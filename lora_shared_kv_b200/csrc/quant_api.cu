@@ -96,7 +96,7 @@ lrkv_status cache_params(const lrkv_problem* p, const lrkv_kv_view* x, int32_t T
 struct QPlan {
   int G, R, n_rg, rows_per_group, n_u_slots, nt, ctas, stages, u_stages, smem, RP;
   long long items;
-  size_t tickets_off, partials_off, bytes;
+  size_t partials_off, bytes;
 };
 
 lrkv_status plan_decode_quant(const lrkv_problem* p, int max_seq_len, const DeviceInfo& dev, QPlan* pl) {
@@ -144,8 +144,7 @@ lrkv_status plan_decode_quant(const lrkv_problem* p, int max_seq_len, const Devi
   if (stages < groups) return fail(LRKV_ERR_UNSUPPORTED, "decode tiles do not fit in shared memory");
   pl->stages = stages;
   pl->smem = smem_of(stages);
-  pl->tickets_off = lrkv::kWsHeaderBytes;
-  pl->partials_off = pl->tickets_off + ((size_t)pl->items * 4 + 255) / 256 * 256;
+  pl->partials_off = lrkv::kWsHeaderBytes + lrkv::kQTicketBytes;
   pl->bytes = pl->partials_off + (size_t)2 * pl->ctas * lrkv::q_record_floats(pl->RP, p->head_dim, p->rank) * 4;
   return LRKV_OK;
 }
@@ -279,7 +278,7 @@ lrkv_status lrkv_attn_decode_quant(const lrkv_problem* p, const void* q, const l
   dp.scale_log2 = scale_of(p) * 1.4426950408889634f;
   char* ws = static_cast<char*>(workspace);
   dp.flags = reinterpret_cast<unsigned*>(ws);
-  dp.tickets = reinterpret_cast<int*>(ws + pl.tickets_off);
+  dp.tickets = reinterpret_cast<unsigned*>(ws + lrkv::kWsHeaderBytes);
   dp.partials = reinterpret_cast<float*>(ws + pl.partials_off);
   take_stall_hook(&dp.spin_cap, &dp.stall);
   s = lrkv::launch_decode_quant(dp, D, RK, pl.rows_per_group, kv->format, &tmK, &tmV, &tmU, pl.smem, pl.ctas, stream);

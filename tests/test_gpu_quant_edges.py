@@ -143,3 +143,49 @@ def test_zero_values_as_written_before_large_ones(fmt):
     v[:, 320:] = _tokens("wr v", 1, 64, 1, 128) * 2.0 ** 30
     c.cache.write(_tokens("wr k", 1, 384, 1, 128), v, 384, None, _i32([340]))
     _check(c, c.run(), fmt)
+
+
+# ---------------------------------------------------------------------------
+# one workspace for several shapes and operators
+# ---------------------------------------------------------------------------
+
+def _wide(seed, fmt="e4m3", S=40):
+    """Many short sessions and a long last one: its items, past the 64th, are split over CTAs."""
+    return DecodeCase(seed, fmt, S, 1, 8, 2, 64, 16, 4000, 1, [0] * S, [1 + i % 70 for i in range(S - 1)] + [4000])
+
+
+def test_a_workspace_serves_a_growing_batch():
+    wide = _wide("grow")
+    want = wide.run()
+    _check(wide, want, "wide")
+    small = [DecodeCase(("grow", n), "int8", n, 2, 4, 1, 128, 32, 6000, 0, [0, 100] * n, [6000] * n)
+             for n in (1, 2, 7)]
+    ws = torch.zeros(max(c.workspace().numel() for c in small + [wide]), dtype=torch.uint8, device=DEV)
+    for c in small:
+        first = c.run()
+        assert torch.equal(c.run(ws=ws), first)
+        assert torch.equal(wide.run(ws=ws), want)
+        assert torch.equal(c.run(ws=ws), first)
+
+
+def test_a_workspace_that_other_operators_used():
+    wide = _wide("others")
+    want = wide.run()
+    S, N, Hq, Hkv, d, r, L = 2, 8, 16, 2, 128, 16, 3000
+    prob = lrkv.make_problem(S, N, Hq, Hkv, d, r)
+    x = torch.randn((2, S, Hkv, L, d), generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).to(DEV)
+    kv = lrkv.kv_view_dense(x[0], x[1])
+    u = torch.randn((S, N, L, r), generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).to(DEV)
+    b = torch.randn((N, r, Hkv * d), generator=torch.Generator().manual_seed(3)).to(torch.bfloat16).to(DEV)
+    T = 128
+    q = torch.randn((N, T, Hq, d), generator=torch.Generator().manual_seed(4)).to(torch.bfloat16).to(DEV)
+    one = torch.empty((S, N, Hq, d), dtype=torch.bfloat16, device=DEV)
+    chunk = torch.empty_like(q)
+    need = [lrkv.lrkv_decode_workspace_bytes(prob, L), lrkv.lrkv_prefill_workspace_bytes(prob, L - T, T)]
+    ws = torch.zeros(max(need + [wide.workspace().numel()]), dtype=torch.uint8, device=DEV)
+    lrkv.lrkv_attn_decode(prob, q[:S, 0].reshape(S, 1, Hq, d).repeat(1, N, 1, 1), kv, _i32([L, L]), L, u, b, None, one,
+                          ws)
+    assert torch.equal(wide.run(ws=ws), want)
+    ws.zero_()
+    lrkv.lrkv_attn_prefill_chunk(prob, q, kv, 0, L - T, T, u, b, None, chunk, ws)
+    assert torch.equal(wide.run(ws=ws), want)
