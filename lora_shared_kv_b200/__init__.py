@@ -296,12 +296,23 @@ def _fits(view, problem, rows, what):
         raise ValueError(f"the {what} view holds [sessions, KV heads, rows, head_dim] {view.holds}, the call needs {need}")
 
 
+def _u_fits(view, problem, rows):
+    """The U view holds the problem's sessions, an agent slot each (one for all in BaseLRShared), `rows` rows, and
+    rows of the problem's rank."""
+    S, n, L, r = view.holds
+    slots = problem.num_agents if problem.mode == BASE_SHARED else 1
+    if S < problem.num_sessions or n < slots or L < rows or r != problem.rank:
+        need = (problem.num_sessions, slots, rows, problem.rank)
+        raise ValueError(f"the U view holds [sessions, agent slots, rows, rank] {view.holds}, the call needs {need}")
+
+
 def u_view(u):
     """u: bf16 [S, N_U, rows, r] with r contiguous."""
     _require(u.dtype == torch.bfloat16 and u.dim() == 4 and u.stride(3) == 1, "u: bf16 [S, N_U, rows, r], r contiguous")
     _on_device(u=u)
     view = UView(u.data_ptr(), u.stride(0), u.stride(1), u.stride(2), u.shape[2])
     view.tensors = (u,)
+    view.holds = tuple(u.shape)
     return view
 
 
@@ -497,8 +508,9 @@ def lrkv_attn_decode_quant(problem, q, kv, seq_lens, max_seq_len, u, b, offsets,
              "b: [num_agents, rank, num_kv_heads * head_dim]")
     max_seq_len = int(max_seq_len)
     _fits(kv, p, max_seq_len, "8-bit")
-    dev = _on_current(q, seq_lens, b, offsets, out, workspace, *kv.tensors)
     uv = u if isinstance(u, UView) else u_view(u)
+    _u_fits(uv, p, max_seq_len)
+    dev = _on_current(q, seq_lens, b, offsets, out, workspace, *kv.tensors, *uv.tensors)
     _check(lib().lrkv_attn_decode_quant(p, q.data_ptr(), kv, seq_lens.data_ptr(), max_seq_len, uv, b.data_ptr(),
                                         _at(offsets), out.data_ptr(), odt, workspace.data_ptr(),
                                         workspace.numel() * workspace.element_size(), _raw_stream(stream, dev)))
