@@ -217,6 +217,11 @@ def make_problem(S, N, Hq, Hkv, d, r, mode=BASE_SHARED, softmax_scale=0.0):
     return Problem(S, N, Hq, Hkv, d, r, mode, softmax_scale)
 
 
+def _both(k, v):
+    """What both tensors hold: the smaller size of each dimension."""
+    return tuple(min(a, b) for a, b in zip(k.shape, v.shape))
+
+
 def kv_view_dense(k, v):
     """k, v: bf16 [S, Hkv, L, d] with d contiguous (same strides)."""
     _require(k.dtype == torch.bfloat16 and v.dtype == torch.bfloat16 and k.dim() == 4, "k, v: bf16 [S, Hkv, L, d]")
@@ -224,22 +229,23 @@ def kv_view_dense(k, v):
     _on_device(k=k, v=v)
     view = KVView(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2), None, 0, 0, 0, 0)
     view.tensors = (k, v)  # a view keeps its tensors alive
-    view.holds = tuple(k.shape)
+    view.holds = _both(k, v)
     return view
 
 
 def kv_view_paged(k_pages, v_pages, page_table):
     """k_pages, v_pages: bf16 [P, Hkv, page, d]; page_table: int32 [S, n_logical_pages] on the device."""
     _require(k_pages.dtype == torch.bfloat16 and v_pages.dtype == torch.bfloat16 and k_pages.dim() == 4
-             and k_pages.stride() == v_pages.stride(), "k_pages, v_pages: bf16 [P, Hkv, page, d], same strides")
+             and k_pages.stride() == v_pages.stride() and k_pages.shape[2:] == v_pages.shape[2:],
+             "k_pages, v_pages: bf16 [P, Hkv, page, d], same strides, same page size and d")
     _require(page_table.dtype == torch.int32 and page_table.dim() == 2 and page_table.stride(1) == 1,
              "page_table: int32 [S, n_logical_pages], rows contiguous")
     _on_device(k_pages=k_pages, v_pages=v_pages, page_table=page_table)
+    pages, heads, page, d = _both(k_pages, v_pages)
     view = KVView(k_pages.data_ptr(), v_pages.data_ptr(), 0, k_pages.stride(1), k_pages.stride(2),
-                  page_table.data_ptr(), page_table.stride(0), k_pages.stride(0), k_pages.shape[2],
-                  k_pages.shape[0])
+                  page_table.data_ptr(), page_table.stride(0), k_pages.stride(0), page, pages)
     view.tensors = (k_pages, v_pages, page_table)
-    view.holds = (page_table.shape[0], k_pages.shape[1], page_table.shape[1] * k_pages.shape[2], k_pages.shape[3])
+    view.holds = (page_table.shape[0], heads, page_table.shape[1] * page, d)
     return view
 
 

@@ -76,3 +76,43 @@ def test_a_us_device_is_checked(monkeypatch):
     with pytest.raises(AssertionError, match="lrkv_attn_decode_quant"):
         _decode(lrkv.u_view(u))
     assert any(t is u for t in seen)
+
+
+# ---------------------------------------------------------------------------
+# bf16 views whose K and V differ
+# ---------------------------------------------------------------------------
+
+def _write(src, T, dst=None):
+    prob = lrkv.make_problem(S, N, Hq, Hkv, d, r)
+    lrkv.lrkv_quantize_kv(prob, src, T, dst or _kv8(), L, None, None, torch.zeros(256, dtype=torch.uint8), stream=0)
+
+
+def _read(dst, T):
+    prob = lrkv.make_problem(S, N, Hq, Hkv, d, r)
+    lrkv.lrkv_dequantize_kv(prob, _kv8(), L, T, dst, None, None, torch.zeros(256, dtype=torch.uint8), stream=0)
+
+
+V_TOO_SMALL = {"sessions": (slice(0, S - 1),), "heads": (slice(None), slice(0, Hkv - 1)),
+               "rows": (slice(None), slice(None), slice(0, 99))}
+
+
+@pytest.mark.parametrize("cut", V_TOO_SMALL.values(), ids=V_TOO_SMALL)
+def test_a_dense_view_holds_what_both_of_its_tensors_hold(cut):
+    k, v = _bf16(S, Hkv, 128, d), _bf16(S, Hkv, 128, d)
+    for view in (lrkv.kv_view_dense(k, v[cut]), lrkv.kv_view_dense(k[cut], v)):
+        for call in (_write, _read):
+            with pytest.raises(ValueError, match="bf16 view holds"):
+                call(view, 100)
+    with pytest.raises(AssertionError, match="lrkv_quantize_kv"):
+        _write(lrkv.kv_view_dense(k, v[:, :, :100]), 100)
+
+
+def test_a_paged_view_holds_what_both_of_its_tensors_hold():
+    k, v, table = _bf16(9, Hkv, 64, d), _bf16(9, Hkv, 64, d), _i32(S, 2)
+    assert lrkv.kv_view_paged(k, v[:5], table).num_pages == 5  # the kernels flag page ids from there on
+    assert lrkv.kv_view_paged(k[:4], v, table).num_pages == 4
+    for call in (_write, _read):
+        with pytest.raises(ValueError, match="bf16 view holds"):
+            call(lrkv.kv_view_paged(k, v[:, :1], table), 100)
+    with pytest.raises(ValueError, match="same page size"):
+        lrkv.kv_view_paged(k, v[:, :, :32], table)
