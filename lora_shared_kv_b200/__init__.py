@@ -294,9 +294,18 @@ def kv_view_quant_paged(k8_pages, v8_pages, k_scale, v_scale, page_table):
     return view
 
 
+def _holds(view, what, made_by):
+    """What a view's buffers hold; a view built by hand does not say."""
+    holds = getattr(view, "holds", None)
+    if holds is None:
+        raise TypeError(f"the {what} view must come from {made_by}, got {type(view).__name__} without its tensors")
+    return holds
+
+
 def _fits(view, problem, rows, what):
     """The view's buffers hold the problem's sessions, KV heads and head_dim, and `rows` rows of each."""
-    S, H, L, d = view.holds
+    S, H, L, d = _holds(view, what, "kv_view_dense or kv_view_paged" if what == "bf16" else
+                        "kv_view_quant_dense or kv_view_quant_paged")
     if S < problem.num_sessions or H < problem.num_kv_heads or L < rows or d != problem.head_dim:
         need = (problem.num_sessions, problem.num_kv_heads, int(rows), problem.head_dim)
         raise ValueError(f"the {what} view holds [sessions, KV heads, rows, head_dim] {view.holds}, the call needs {need}")
@@ -305,7 +314,7 @@ def _fits(view, problem, rows, what):
 def _u_fits(view, problem, rows):
     """The U view holds the problem's sessions, an agent slot each (one for all in BaseLRShared), `rows` rows, and
     rows of the problem's rank."""
-    S, n, L, r = view.holds
+    S, n, L, r = _holds(view, "U", "u_view")
     slots = problem.num_agents if problem.mode == BASE_SHARED else 1
     if S < problem.num_sessions or n < slots or L < rows or r != problem.rank:
         need = (problem.num_sessions, slots, rows, problem.rank)

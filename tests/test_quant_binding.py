@@ -116,3 +116,22 @@ def test_a_paged_view_holds_what_both_of_its_tensors_hold():
             call(lrkv.kv_view_paged(k, v[:, :1], table), 100)
     with pytest.raises(ValueError, match="same page size"):
         lrkv.kv_view_paged(k, v[:, :, :32], table)
+
+
+# ---------------------------------------------------------------------------
+# views built by hand
+# ---------------------------------------------------------------------------
+
+def test_views_without_their_tensors_are_refused_with_a_message():
+    kv = lrkv.KVView(0x1000, 0x1000, Hkv * L * d, L * d, d, None, 0, 0, 0, 0)
+    kv8 = lrkv.QKVView(0x1000, 0x1000, 0x1000, 0x1000, Hkv * L * d, L * d, d, 8, 4)
+    uv = lrkv.UView(0x1000, N * L * r, L * r, r, L)
+    held = lrkv.kv_view_dense(_bf16(S, Hkv, 8, d), _bf16(S, Hkv, 8, d))
+    for call in (lambda: _write(kv, 8), lambda: _read(kv, 8)):
+        with pytest.raises(TypeError, match="kv_view_dense or kv_view_paged"):
+            call()
+    for call in (lambda: _write(held, 8, dst=kv8), lambda: _decode(_bf16(S, N, L, r), kv=kv8)):
+        with pytest.raises(TypeError, match="kv_view_quant_dense or kv_view_quant_paged"):
+            call()
+    with pytest.raises(TypeError, match="u_view"):
+        _decode(uv)
