@@ -444,7 +444,8 @@ typedef struct {
  * one session.  A session with a negative first row or count, a count above T
  * or rows past dst_rows is flagged on the device and not written; a block with
  * a page id out of range (in src or dst) likewise.  p->num_agents, num_q_heads
- * and rank play no part but must be valid.  T == 0 is a no-op.
+ * and rank play no part but must be valid.  T == 0 is a no-op (src may then be
+ * a view of no rows, with null pointers).
  */
 lrkv_status lrkv_quantize_kv(const lrkv_problem* p, const lrkv_kv_view* src, int32_t T, const lrkv_qkv_view* dst,
                              int32_t dst_rows, const int32_t* first_rows, const int32_t* row_counts,

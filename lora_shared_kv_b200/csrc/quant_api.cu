@@ -36,13 +36,13 @@ lrkv_status check_qkv(const lrkv_qkv_view* v, const lrkv_problem* p) {
   return LRKV_OK;
 }
 
-// Checks and parameters shared by the write (to_quant) and the read.
+// Checks and parameters (none if T is 0) shared by the write and the read.
 lrkv_status cache_params(const lrkv_problem* p, const lrkv_kv_view* x, int32_t T, const lrkv_qkv_view* c, int32_t rows,
                          const int32_t* first, const int32_t* count, void* workspace, size_t workspace_bytes,
                          lrkv::QCacheParams* out) {
   lrkv_status s = check_problem(p);
   if (s != LRKV_OK) return s;
-  if ((s = check_kv(x, p)) != LRKV_OK) return s;
+  if (T != 0 && (s = check_kv(x, p)) != LRKV_OK) return s;  // tensors of no rows have no address
   if ((s = check_qkv(c, p)) != LRKV_OK) return s;
   if (!workspace) return fail(LRKV_ERR_INVALID_ARGUMENT, "workspace must not be NULL");
   if (!aligned16(workspace)) return fail(LRKV_ERR_MISALIGNED, "workspace must be 16-byte aligned");
@@ -52,6 +52,7 @@ lrkv_status cache_params(const lrkv_problem* p, const lrkv_kv_view* x, int32_t T
   if (rows > kMaxRows) return fail(LRKV_ERR_UNSUPPORTED, "more than %d rows a session", kMaxRows);
   if (T > rows && !count) return fail(LRKV_ERR_INVALID_ARGUMENT, "%d rows exceed the 8-bit cache's %d", T, rows);
   if (T > kMaxRows) return fail(LRKV_ERR_UNSUPPORTED, "T %d", T);
+  if (T == 0) return LRKV_OK;
   if (c->page_table && ((long long)rows + LRKV_QUANT_BLOCK - 1) / LRKV_QUANT_BLOCK > c->page_table_stride)
     return fail(LRKV_ERR_INVALID_ARGUMENT, "%d rows exceed a page-table row of %lld pages", rows, (long long)c->page_table_stride);
   if (x->page_table && ((long long)T + LRKV_QUANT_BLOCK - 1) / LRKV_QUANT_BLOCK > x->page_table_stride)
