@@ -453,7 +453,8 @@ lrkv_status lrkv_quantize_kv(const lrkv_problem* p, const lrkv_kv_view* src, int
 
 /*
  * Read an 8-bit cache back: rows [0, n) of session s of `dst` (bf16, dense or
- * paged) take code * scale, rounded to nearest even bf16, of rows [f, f + n) of
+ * paged) take code * scale, rounded to nearest even bf16 (int8 codes of values
+ * next to bf16's largest may round to infinity), of rows [f, f + n) of
  * session s of `src`; f, n, T and the workspace as in lrkv_quantize_kv.  Rows
  * of dst past n are left as they were.  The prefill chunk over an 8-bit cache
  * is this call into a bf16 staging cache, then lrkv_attn_prefill_chunk.
@@ -477,11 +478,13 @@ size_t lrkv_decode_quant_workspace_bytes(const lrkv_problem* p, int32_t max_seq_
  *   out[s,i,h,:] = sum_{t < seq_lens[s]} P[t] (cv[t] sv[t/64] + [t >= a_{s,i}] U_i[t] B_i,g)
  *   P = softmax(q[s,i,h] . ck[t] sk[t/64] * scale)
  * with codes c and scales s of the cache.  Other arguments as lrkv_attn_decode.
- * Numerics: codes enter the tensor cores exactly, as fp16; q exactly (scaled by a
- * power of two per row); softmax statistics, scores and accumulators in fp32;
- * the weights enter the value product as fp16 (times the block's value scale,
- * against a running reference, so no weight of a long context underflows) and
- * the low-rank product as bf16.  Codes, scales and U rows at or past seq_len and U
+ * Numerics: codes enter the tensor cores exactly, as fp16; q too (scaled by a
+ * power of two per row), exactly down to 2^-28 of the row's largest element;
+ * softmax statistics, scores and accumulators in fp32; the weights enter the
+ * value product as fp16 (times the block's value scale, against a running
+ * reference, so no weight of a long context underflows, whatever the scales) and
+ * the low-rank product as bf16.  A weight below 2^-126 of its row's largest may
+ * count as zero.  Codes, scales and U rows at or past seq_len and U
  * rows before a_i may hold anything, NaN included.
  * A NaN or infinity in a U row that counts for one agent may reach the outputs of
  * other agents of the call, as in lrkv_attn_decode.

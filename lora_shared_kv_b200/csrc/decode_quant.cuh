@@ -13,12 +13,15 @@
 //    730 cycles, and has to turn its 16 K codes into fp16: a conversion per two codes
 //    at half rate, 128 cycles, and per 16 rows 128 MMAs of m16n8k16 at 2 cycles, 256
 //    cycles.  (The warp-level fp8 MMA measured 6.2 cycles against 3.3 for fp16 MMA and
-//    conversions together, and would round q and p to 4 bits.)  Measured: 4 x 64k paged,
-//    8 agents, 117 us (floor 85); 32 x 8k, 18 rows, e4m3 52 us and int8 58 (floor 21);
-//    16 x 1k, 4 rows, 14.8 us (floor 5.3).  A launch takes about 7 us until its first
-//    tile has landed and 4 to 7 us from the last tile to the output, which is what
-//    separates the shorter ones from their floor; at 18 rows the warps' latency chains
-//    (3,000 cycles for 32 keys) hold the ring as well.
+//    conversions together, and would round q and p to 4 bits.)  Measured (e4m3 / int8, in
+//    brackets the decode over the same cache in bf16): 4 x 64k paged, 16 rows, 117.5 / 137
+//    us (188; floor 85); 32 x 8k, 18 rows, 54.6 / 58.7 us (58.2; floor 21); 16 x 1k, 4
+//    rows, 14.9 / 16.2 us (17.1; floor 5.3).  A tile without low-rank work takes 623 / 721
+//    cycles at 8 rows on 128 CTAs (630 is the HBM rate there), 675 / 804 at 16, 993 /
+//    1,156 at 18 and 1,210 / 1,493 at 32: up to 8 rows the HBM bounds, at 16 nearly so, from
+//    17 on the consumers.  A launch takes about 7 us until its first tile has landed and 4 to
+//    7 us from the last tile to the output, which is what separates the shorter ones
+//    from their floor.
 //  * A warp holds ALL rows of its row block (8, 16 or 16 + 8) and a slice of the
 //    tile's keys, so that a code is converted once per tile.  The 16-row part
 //    has rows as the MMA's M, the 8-row part has keys (or dims) as M; the
